@@ -23,7 +23,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfh.so")
 
 FH_OK, FH_ERR_ARG, FH_ERR_SHAPE, FH_ERR_CUDA, FH_ERR_OOM, FH_ERR_TIMEOUT, FH_ERR_UNSUPPORTED = 0, -1, -2, -3, -4, -5, -6
-FH_F32, FH_BF16 = 0, 1
+FH_F32, FH_BF16, FH_MXFP8, FH_MXFP4 = 0, 1, 2, 3
+FH_ACT_NONE, FH_ACT_GELU = 0, 1
 ERROR_NAMES = {0: "FH_OK", -1: "FH_ERR_ARG", -2: "FH_ERR_SHAPE", -3: "FH_ERR_CUDA", -4: "FH_ERR_OOM",
                -5: "FH_ERR_TIMEOUT", -6: "FH_ERR_UNSUPPORTED"}
 
@@ -112,6 +113,12 @@ def load_library() -> ctypes.CDLL:
         "fh_op_attention": (I, [P, P, P, P, P, I, I, I, F, I, P]),
         "fh_op_cross_attention": (I, [P, P, P, P, P, I, I, I, I, I, F, I, P]),
         "fh_op_row_norm": (I, [P, P, I, I, I, P, P, ctypes.c_long, I, F, I, P]),
+        "fh_mx_data_bytes": (Z, [I, I, I]),
+        "fh_mx_scale_bytes": (Z, [I, I]),
+        "fh_op_quantize": (I, [P, ctypes.c_long, I, I, I, I, P, P, P]),
+        "fh_op_dequantize": (I, [P, P, I, I, I, P, I, P]),
+        "fh_op_add_rms_norm": (I, [P, I, P, I, P, P, P, ctypes.c_long, I, I, I, F, I, P, P, P]),
+        "fh_op_linear_mx": (I, [P, P, P, P, P, I, I, I, I, I, I, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -324,5 +331,262 @@ def attention(q, k, v, ssq, eps=1e-6, stream=None):
     return out
 
 
+# ------------------------------------------------------------------ microscaled operators
+FORMATS = {"mxfp8": FH_MXFP8, "mxfp4": FH_MXFP4}
+
+
+class MXTensor:
+    """A microscaled matrix: ``shape`` (rows, columns) values as element codes and one
+    power-of-two scale per 32 columns (the layout: include/fh_ops.h).
+
+    ``data``: uint8 [rows, columns] (``fmt`` "mxfp8", e4m3) or [rows, columns / 2] ("mxfp4",
+    e2m1, two to a byte); ``scales``: the flat uint8 tiles, `scale_bytes` long, zero past the
+    tensor's rows and blocks."""
+
+    __slots__ = ("data", "scales", "shape", "fmt")
+
+    def __init__(self, data, scales, shape, fmt):
+        self.data, self.scales, self.shape, self.fmt = data, scales, shape, fmt
+
+    @staticmethod
+    def scale_bytes(rows: int, cols: int) -> int:
+        return -(-rows // 128) * -(-cols // 128) * 512
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, fmt: str, device) -> "MXTensor":
+        """Room for rows x cols values, not initialised."""
+        import torch
+        _format(fmt)
+        data = torch.empty((rows, cols if fmt == "mxfp8" else cols // 2), dtype=torch.uint8, device=device)
+        scales = torch.empty(cls.scale_bytes(rows, cols), dtype=torch.uint8, device=device)
+        return cls(data, scales, (rows, cols), fmt)
+
+    @property
+    def device(self):
+        return self.data.device
+
+    def __repr__(self):
+        return f"MXTensor({self.shape[0]} x {self.shape[1]}, {self.fmt}, {self.device})"
+
+
+def _format(fmt) -> int:
+    code = FORMATS.get(fmt)
+    if code is None:
+        raise ValueError(f"format {fmt!r}: expected one of {sorted(FORMATS)}")
+    return code
+
+
+def _dtype(t, what: str) -> int:
+    import torch
+    if t.dtype == torch.float32:
+        return FH_F32
+    if t.dtype == torch.bfloat16:
+        return FH_BF16
+    raise TypeError(f"{what}: expected float32 or bfloat16, got {t.dtype}")
+
+
+def _cuda_tensor(t, what: str, device=None):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, expected cuda:{device}")
+    return t
+
+
+def _matrix(t, what: str, device=None):
+    """A contiguous 2-D CUDA tensor."""
+    _cuda_tensor(t, what, device)
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected 2 dimensions, got {t.dim()}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t
+
+
+def _mx_operand(q, what: str, device=None) -> int:
+    """Checks a microscaled operand; returns its format code."""
+    import torch
+    if not isinstance(q, MXTensor):
+        raise TypeError(f"{what}: expected an MXTensor")
+    code = _format(q.fmt)
+    rows, cols = q.shape
+    if rows < 1 or cols < 32 or cols % 32:
+        raise ValueError(f"{what}: {rows} x {cols} is not a microscaled shape (columns: a multiple of 32)")
+    for t, n, name in ((q.data, rows * cols // (2 if code == FH_MXFP4 else 1), "data"),
+                       (q.scales, MXTensor.scale_bytes(rows, cols), "scales")):
+        _cuda_tensor(t, what, device)
+        if t.dtype != torch.uint8 or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{what}.{name}: expected {n} contiguous uint8 values")
+        device = t.get_device()
+    return code
+
+
+def _launch(device: int, stream, inputs, call):
+    """``call(handle)`` with `device` current and its outputs allocated on the launching stream:
+    torch's current stream of that device, or `stream` (a torch stream or a handle), for which
+    the inputs' memory is then kept until its work is done."""
+    import torch
+    if stream is None:
+        if torch.cuda.current_device() == device:
+            return call(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(device):
+            return call(torch.cuda.current_stream().cuda_stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
+    if stream.device_index != device:
+        raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the tensors to cuda:{device}")
+    with torch.cuda.stream(stream):  # makes the stream's device current too
+        out = call(stream.cuda_stream)
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+    return out
+
+
+def _result(rows: int, cols: int, out, device):
+    """An output of the asked type, its type code and the pointers of its two parts."""
+    import torch
+    if out is torch.bfloat16 or out is torch.float32:
+        t = torch.empty((rows, cols), dtype=out, device=device)
+        return t, FH_BF16 if out is torch.bfloat16 else FH_F32, t.data_ptr(), None
+    q = MXTensor.empty(rows, cols, out, device)
+    return q, FORMATS[out], q.data.data_ptr(), q.scales.data_ptr()
+
+
+def _out_type(out):
+    import torch
+    if out is not torch.bfloat16 and out is not torch.float32 and out not in FORMATS:
+        raise ValueError(f"out={out!r}: expected torch.float32, torch.bfloat16, 'mxfp8' or 'mxfp4'")
+
+
+def quantize(x, fmt="mxfp8", stream=None):
+    """The microscaled form of x [rows, columns] (float32 or bfloat16): an MXTensor.
+
+    Columns are a multiple of 32 and contiguous; rows may be any multiple of 16 bytes apart.
+    Each block's scale is the smallest power of two (2^-127 or more) under which nothing in it
+    saturates; elements round to nearest, ties to even. A block with an infinity or a NaN reads
+    back as NaN."""
+    code = _format(fmt)
+    _cuda_tensor(x, "x")
+    dt = _dtype(x, "x")
+    if x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError("x: expected 2 dimensions with contiguous rows")
+    M, K = x.shape
+    ld = x.stride(0) if M > 1 else K
+    dev = x.get_device()
+
+    def call(handle):
+        q = MXTensor.empty(M, K, fmt, x.device)
+        _check(load_library().fh_op_quantize(x.data_ptr(), ld, M, K, dt, code, q.data.data_ptr(), q.scales.data_ptr(),
+                                             handle))
+        return q
+
+    return _launch(dev, stream, (x,), call)
+
+
+def dequantize(q, dtype=None, stream=None):
+    """The values of a microscaled tensor, float32 (the default) or bfloat16 [rows, columns]."""
+    import torch
+    code = _mx_operand(q, "q")
+    dtype = dtype or torch.float32
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"dtype: expected float32 or bfloat16, got {dtype}")
+    M, K = q.shape
+
+    def call(handle):
+        out = torch.empty((M, K), dtype=dtype, device=q.device)
+        _check(load_library().fh_op_dequantize(q.data.data_ptr(), q.scales.data_ptr(), M, K, code, out.data_ptr(),
+                                               FH_BF16 if dtype == torch.bfloat16 else FH_F32, handle))
+        return out
+
+    return _launch(q.data.get_device(), stream, (q.data, q.scales), call)
+
+
+def add_rms_norm(x, res, a, c=None, out="mxfp8", eps=1e-6, sum_out=None, stream=None):
+    """(sum, y): sum = x + res in x's type, and its RMS norm y in the type that `out` names
+    (torch.float32, torch.bfloat16, "mxfp8" or "mxfp4").
+
+    With n = sum / sqrt(mean(sum^2) + eps) per row: y = n * a, or n * (1 + a) + c. x and res
+    [rows, columns] are float32 or bfloat16 each; a and c float32 vectors of a row's width, or
+    [streams, columns] where each of `streams` equal runs of rows has its own. Columns are a
+    multiple of 32, at most 16384. The sum goes to a new tensor, or to `sum_out`, which may be x
+    itself (or res, where the types agree)."""
+    import torch
+    _out_type(out)
+    _matrix(x, "x")
+    dev = x.get_device()
+    _matrix(res, "res", dev)
+    M, D = x.shape
+    if res.shape != x.shape:
+        raise ValueError(f"res: expected shape {tuple(x.shape)}, got {tuple(res.shape)}")
+    _cuda_tensor(a, "a", dev)
+    streams = a.shape[0] if a.dim() == 2 else 1
+    if a.dtype != torch.float32 or a.dim() not in (1, 2) or a.shape[-1] != D or not a.is_contiguous():
+        raise ValueError(f"a: expected contiguous float32 [{D}] or [streams, {D}]")
+    if streams < 1 or M % streams:
+        raise ValueError(f"{M} rows do not divide into {streams} streams")
+    if c is not None:
+        _cuda_tensor(c, "c", dev)
+        if c.dtype != torch.float32 or c.shape != a.shape or not c.is_contiguous():
+            raise ValueError("c: expected a contiguous float32 tensor of a's shape")
+    if sum_out is not None:
+        _matrix(sum_out, "sum_out", dev)
+        if sum_out.shape != x.shape or sum_out.dtype != x.dtype:
+            raise ValueError("sum_out: expected x's shape and type")
+    xt, rt = _dtype(x, "x"), _dtype(res, "res")
+
+    def call(handle):
+        total = torch.empty_like(x) if sum_out is None else sum_out
+        y, kind, data, scales = _result(M, D, out, x.device)
+        _check(load_library().fh_op_add_rms_norm(x.data_ptr(), xt, res.data_ptr(), rt, total.data_ptr(), a.data_ptr(),
+                                                 None if c is None else c.data_ptr(), D if streams > 1 else 0,
+                                                 max(1, M // streams), M, D, eps, kind, data, scales, handle))
+        return total, y
+
+    return _launch(dev, stream, (x, res, a, c, sum_out), call)
+
+
+def linear_mx(A, W, bias=None, act=None, out=None, stream=None):
+    """act(A @ W^T + bias) of two MXTensors of one format, on the block-scaled tensor core.
+
+    A is rows x K, W columns x K, bias float32 [columns] or None, act None or "gelu" (the tanh
+    form). The result has the type that `out` names: torch.bfloat16 (the default),
+    torch.float32, or "mxfp8" / "mxfp4" (columns a multiple of 32), an operand of the next
+    product; sums are kept in float32."""
+    import torch
+    out = torch.bfloat16 if out is None else out
+    _out_type(out)
+    if act not in (None, "gelu"):
+        raise ValueError(f"act={act!r}: expected None or 'gelu'")
+    code = _mx_operand(A, "A")
+    dev = A.data.get_device()
+    if _mx_operand(W, "W", dev) != code:
+        raise ValueError(f"A is {A.fmt}, W is {W.fmt}: expected one format")
+    (M, K), (N, KW) = A.shape, W.shape
+    if K != KW:
+        raise ValueError(f"A has {K} columns, W has {KW}")
+    if bias is not None:
+        _cuda_tensor(bias, "bias", dev)
+        if bias.dtype != torch.float32 or bias.shape != (N,) or not bias.is_contiguous():
+            raise ValueError(f"bias: expected contiguous float32 [{N}]")
+    if out in FORMATS and N % 32:
+        raise ValueError(f"{N} columns: a microscaled output needs a multiple of 32")
+
+    def call(handle):
+        y, kind, data, scales = _result(M, N, out, A.device)
+        _check(load_library().fh_op_linear_mx(A.data.data_ptr(), A.scales.data_ptr(), W.data.data_ptr(),
+                                              W.scales.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K,
+                                              code, FH_ACT_NONE if act is None else FH_ACT_GELU, kind, data, scales,
+                                              handle))
+        return y
+
+    return _launch(dev, stream, (A.data, A.scales, W.data, W.scales, bias), call)
+
+
 __all__ = ["DiT", "ModelConfig", "LITE", "FP32_BLOCK", "ONE_BLOCK", "LITE_768_X3", "FHError", "load_library",
-           "linear", "attention", "cross_attention", "row_norm", "FH_F32", "FH_BF16"]
+           "linear", "attention", "cross_attention", "row_norm", "MXTensor", "quantize", "dequantize", "add_rms_norm",
+           "linear_mx", "FH_F32", "FH_BF16", "FH_MXFP8", "FH_MXFP4"]

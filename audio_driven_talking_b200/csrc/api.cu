@@ -109,6 +109,26 @@ bool make_qkv_map(CUtensorMap* map, const void* base, uint64_t L, uint64_t plane
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Microscaled operand of the block-scaled product: its codes as bytes [rows][pitch], box 128
+// bytes x box_rows, 128-byte swizzle, and its scale tiles as 32-bit words [row tiles][K tiles]
+// [128], box 128 x box_kt x box_rt. What a box reads past either end is zero.
+bool make_mx_maps(CUtensorMap* codes, CUtensorMap* scales, const void* data, const void* sc, uint64_t rows,
+                  uint64_t pitch, uint64_t K, uint32_t box_rows, uint32_t box_kt, uint32_t box_rt) {
+  cuuint64_t dims[2] = {pitch, rows};
+  cuuint64_t strides[1] = {pitch};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint64_t sdims[3] = {128, (K + 127) / 128, (rows + 127) / 128};
+  cuuint64_t sstrides[2] = {512, 512 * sdims[1]};
+  cuuint32_t sbox[3] = {128, box_kt, box_rt};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(data), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+         g_encode(scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(sc), sdims, sstrides, sbox, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // output map of a CTA-pair GEMM epilogue
 bool epi_out_map(CUtensorMap* map, int kind, bool out_bf16, const EpiParams& ep, int M, int N) {
   if (kind == EPI_QKV)
@@ -626,6 +646,7 @@ int prepare_device(int dev) {
   if (e == cudaSuccess) e = attn_tc_prepare();
   if (e == cudaSuccess) e = cross_attn_prepare();
   if (e == cudaSuccess) e = xattn_tc_prepare();
+  if (e == cudaSuccess) e = gemm_mx_prepare();
   if (e != cudaSuccess) return fail(FH_ERR_CUDA, "kernel attribute setup: %s", cudaGetErrorString(e));
   g_prepared[dev] = true;
   return FH_OK;
@@ -1325,6 +1346,108 @@ int fh_op_attention(const void* q, const void* k, const void* v, const float* ss
     return fail(FH_ERR_ARG, "bad dtype");
   }
   if (e != cudaSuccess) return fail(FH_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
+  return FH_OK;
+}
+
+// ------------------------------------------------------------ microscaled operators
+static bool mx_type(int t) { return t == FH_MXFP8 || t == FH_MXFP4; }
+static bool plain_type(int t) { return t == FH_F32 || t == FH_BF16; }
+static bool mx_shape(int M, int K) { return M >= 1 && M <= 1 << 27 && K >= 32 && K <= 1 << 20 && K % 32 == 0; }
+static int mx_fmt(int t) { return t == FH_MXFP4; }
+static bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+size_t fh_mx_data_bytes(int M, int K, int mxtype) {
+  if (!mx_type(mxtype) || !mx_shape(M, K)) return 0;
+  return (size_t)M * K / (mxtype == FH_MXFP4 ? 2 : 1);
+}
+
+size_t fh_mx_scale_bytes(int M, int K) {
+  if (!mx_shape(M, K)) return 0;
+  return ((size_t)M + 127) / 128 * ((K + 127) / 128) * 512;
+}
+
+// an output's type, and its scales' pointer, which microscaled types alone have
+static int check_out(int out_type, const void* out, const void* out_scales) {
+  if (!plain_type(out_type) && !mx_type(out_type)) return fail(FH_ERR_ARG, "bad output type %d", out_type);
+  if (!out || !aligned16(out) || (mx_type(out_type) ? !out_scales || !aligned16(out_scales) : out_scales != nullptr))
+    return fail(FH_ERR_ARG, "output: null or unaligned pointer, or scales with a type that has none");
+  return FH_OK;
+}
+
+int fh_op_quantize(const void* x, long ldx, int M, int K, int dtype, int mxtype, void* data, void* scales,
+                   void* stream) {
+  if (!x || !data || !scales || !aligned16(x) || !aligned16(data) || !aligned16(scales))
+    return fail(FH_ERR_ARG, "null or unaligned pointer");
+  if (!plain_type(dtype) || !mx_type(mxtype)) return fail(FH_ERR_ARG, "bad dtype");
+  if (!mx_shape(M, K)) return fail(FH_ERR_SHAPE, "%d x %d: K must be a multiple of 32", M, K);
+  if (ldx < K || ldx % (dtype == FH_F32 ? 4 : 8) || ldx > 1L << 40)
+    return fail(FH_ERR_SHAPE, "row stride %ld of %d columns: at least K, and a multiple of 16 bytes", ldx, K);
+  cudaError_t e = mx_quantize(x, ldx, M, K, dtype == FH_BF16, mx_fmt(mxtype), data, scales,
+                              reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(FH_ERR_CUDA, "quantize launch: %s", cudaGetErrorString(e));
+  return FH_OK;
+}
+
+int fh_op_dequantize(const void* data, const void* scales, int M, int K, int mxtype, void* out, int dtype,
+                     void* stream) {
+  if (!data || !scales || !out || !aligned16(data) || !aligned16(scales) || !aligned16(out))
+    return fail(FH_ERR_ARG, "null or unaligned pointer");
+  if (!plain_type(dtype) || !mx_type(mxtype)) return fail(FH_ERR_ARG, "bad dtype");
+  if (!mx_shape(M, K)) return fail(FH_ERR_SHAPE, "%d x %d: K must be a multiple of 32", M, K);
+  cudaError_t e = mx_dequantize(data, scales, M, K, mx_fmt(mxtype), out, dtype == FH_BF16,
+                                reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(FH_ERR_CUDA, "dequantize launch: %s", cudaGetErrorString(e));
+  return FH_OK;
+}
+
+int fh_op_add_rms_norm(const void* x, int x_dtype, const void* res, int res_dtype, void* sum, const float* a,
+                       const float* c, long bstride, int rows_per_batch, int M, int D, float eps, int out_type,
+                       void* out, void* out_scales, void* stream) {
+  if (!x || !res || !sum || !a || !aligned16(x) || !aligned16(res) || !aligned16(sum) || !aligned16(a) || !aligned16(c))
+    return fail(FH_ERR_ARG, "null or unaligned pointer");
+  if (!plain_type(x_dtype) || !plain_type(res_dtype)) return fail(FH_ERR_ARG, "bad dtype");
+  RUN(check_out(out_type, out, out_scales));
+  if (!(eps >= 0.f)) return fail(FH_ERR_ARG, "eps must not be negative");
+  if (!mx_shape(M, D) || D > 16384) return fail(FH_ERR_SHAPE, "%d x %d: D must be a multiple of 32, at most 16384", M, D);
+  if (rows_per_batch < 1 || bstride < 0 || bstride % 4) return fail(FH_ERR_SHAPE, "bad row-norm arguments");
+  const size_t xb = (size_t)M * D * (x_dtype == FH_F32 ? 4 : 2), rb = (size_t)M * D * (res_dtype == FH_F32 ? 4 : 2);
+  if ((sum != x && overlaps(sum, xb, x, xb)) || ((sum != res || res_dtype != x_dtype) && overlaps(sum, xb, res, rb)))
+    return fail(FH_ERR_ARG, "the sum overlaps an input");
+  cudaError_t e = add_rms_norm(x, x_dtype == FH_BF16, res, res_dtype == FH_BF16, sum, a, c, bstride, rows_per_batch, M,
+                               D, eps, out_type, out, out_scales, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(FH_ERR_CUDA, "add-RMS-norm launch: %s", cudaGetErrorString(e));
+  return FH_OK;
+}
+
+int fh_op_linear_mx(const void* A, const void* A_scales, const void* W, const void* W_scales, const float* bias,
+                    int M, int N, int K, int mxtype, int act, int out_type, void* out, void* out_scales,
+                    void* stream) {
+  if (!A || !A_scales || !W || !W_scales || !aligned16(A) || !aligned16(A_scales) || !aligned16(W) ||
+      !aligned16(W_scales) || !aligned16(bias))
+    return fail(FH_ERR_ARG, "null or unaligned pointer");
+  if (!mx_type(mxtype)) return fail(FH_ERR_ARG, "bad operand type %d", mxtype);
+  if (act != FH_ACT_NONE && act != FH_ACT_GELU) return fail(FH_ERR_ARG, "bad activation %d", act);
+  RUN(check_out(out_type, out, out_scales));
+  if (!mx_shape(M, K) || N < 1 || N > 1 << 20) return fail(FH_ERR_SHAPE, "bad product shape %d x %d x %d", M, N, K);
+  if (mx_type(out_type) && N % 32) return fail(FH_ERR_SHAPE, "N = %d: a microscaled output needs a multiple of 32", N);
+  if (!load_encode()) return fail(FH_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled unavailable");
+  int dev = 0, sms = 148;
+  CK(cudaGetDevice(&dev));
+  RUN(prepare_device(dev));
+  CK(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  const MxTile t = gemm_mx_tile(M, N, K, sms);
+  const uint64_t pitch = mxtype == FH_MXFP4 ? K / 2 : K;
+  const uint32_t kt = mxtype == FH_MXFP4 ? 2 : 1;
+  MxMaps maps;
+  if (!make_mx_maps(&maps.a, &maps.sa, A, A_scales, M, pitch, K, 128, kt, 1) ||
+      !make_mx_maps(&maps.w, &maps.sw, W, W_scales, N, pitch, K, t.pair ? t.bn / 2 : t.bn, kt, (t.bn + 127) / 128))
+    return fail(FH_ERR_CUDA, "tensor map encoding");
+  cudaError_t e = gemm_mx(maps, t, bias, out, out_scales, M, N, K, mx_fmt(mxtype), act == FH_ACT_GELU, out_type, sms,
+                          reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(FH_ERR_CUDA, "microscaled linear launch: %s", cudaGetErrorString(e));
   return FH_OK;
 }
 

@@ -1,0 +1,574 @@
+// gemm_mx.cu - block-scaled tensor-core product of two microscaled operands (format: mx.cuh):
+// out[m, n] = act(sum_k A[m, k] W[n, k] + bias[n]), fp32 accumulation, sm_100a.
+//
+// tcgen05.mma ... block_scale multiplies the raw e4m3 or e2m1 codes and applies the e8m0 scales
+// inside the tensor core, from TMEM: A's 128 rows x 4 blocks take 4 TMEM columns (row r in lane
+// r % 32, column r / 32, the 4 blocks its 4 bytes, repeated in every lane quarter), the layout
+// that tcgen05.cp.32x128b.warpx4 makes of one 512-byte scale tile. Both formats run the same
+// loop on 128-byte rows of codes, 128 values of mxfp8 or 256 of mxfp4, four MMAs of 32 bytes:
+//   warp 0     TMA producer: per stage the codes of A and W (128-byte swizzle) and their scale
+//              tiles (zero past the tensor, so a scale that the codes' padding meets is finite).
+//   warp 1     allocates TMEM; one thread copies a stage's scales to TMEM and issues the MMAs.
+//              The scale columns are double-buffered: a copy waits for the MMAs that read its
+//              buffer, so the tensor core always has a stage's MMAs queued.
+//   warps 2-9  epilogue, two warps per TMEM lane quarter, each half of the tile's columns: bias,
+//              GELU, and fp32 or bf16 rows, or the microscaled form again: a thread holds 32
+//              consecutive values of a row, which is a block.
+// Every wait is bounded (FH_WAIT_LIMIT_NS), as in gemm_tc.cu.
+#include <type_traits>
+
+#include "kernels.h"
+#include "mx.cuh"
+
+namespace fh {
+
+namespace {
+
+constexpr int MXG_THREADS = 320;
+constexpr int EPI_THREADS = 256;
+
+template <MxFormat F, int BN, bool PAIR>
+struct MxShape {
+  static constexpr int TM = PAIR ? 256 : 128;
+  static constexpr int KB = F == MX_FP8 ? 128 : 256;  // values per 128-byte row of a stage
+  static constexpr int ATOMS = KB / 128;              // scale tiles along K per stage
+  static constexpr int WROWS = PAIR ? BN / 2 : BN;    // W rows each CTA loads
+  static constexpr int SFBT = (BN + 127) / 128;       // scale row tiles of W
+  static constexpr uint32_t A_BYTES = 128 * 128;
+  static constexpr uint32_t B_BYTES = WROWS * 128;
+  static constexpr uint32_t SFA_BYTES = ATOMS * 512;
+  static constexpr uint32_t SFB_BYTES = SFBT * ATOMS * 512;
+  static constexpr uint32_t OPER_BYTES = A_BYTES + B_BYTES;
+  static constexpr uint32_t SF_BYTES = SFA_BYTES + SFB_BYTES;
+  static constexpr uint32_t STAGE_BYTES = OPER_BYTES + SF_BYTES;
+  static constexpr uint32_t TX_BYTES = STAGE_BYTES * (PAIR ? 2 : 1);
+  static constexpr uint32_t AUX_BYTES = 1024;
+  static constexpr int FIT = (int)((227u * 1024u - 1024u - AUX_BYTES) / STAGE_BYTES);
+  static constexpr int STAGES = FIT < 8 ? FIT : 8;
+  static constexpr uint32_t SF_OFF = STAGES * OPER_BYTES;
+  static constexpr uint32_t AUX_OFF = STAGES * STAGE_BYTES;
+  static constexpr uint32_t SMEM = AUX_OFF + AUX_BYTES + 1024;
+  // TMEM columns: two accumulators (at BN = 256 the second starts inside the first: see the
+  // epilogue), then the scale buffers
+  static constexpr int ACC1 = BN == 256 ? 192 : BN;
+  static constexpr int OVERLAP = BN == 256 ? 64 : 0;
+  static constexpr int SF_COL = ACC1 + BN;
+  static constexpr int SFA_COLS = 4 * ATOMS;
+  static constexpr int SF_COLS = SFA_COLS + 4 * ATOMS * SFBT;
+  static constexpr int NSF = 2;
+  static constexpr uint32_t TMEM_COLS = 512;
+  static_assert(SF_COL + NSF * SF_COLS <= 512, "TMEM");
+  static_assert(STAGES > NSF, "a scale buffer's stage is still in the ring when it is reused");
+};
+
+// Matrix descriptor of a 512-byte scale tile for tcgen05.cp: 16-byte rows, no swizzle, groups
+// of 8 rows 128 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1u << 46;
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tc_cp_scales(uint32_t tmem, uint64_t desc) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+// Instruction descriptor of the block-scaled kinds, e8m0 scales, shape M x N; `id` is the first
+// of the scale bytes (of the 4 of a TMEM column) that this MMA uses, of A and of B.
+__host__ __device__ constexpr uint32_t idesc_mx(MxFormat f, int M, int N, int id) {
+  const uint32_t t = f == MX_FP8 ? 0u : 1u;  // e4m3 in kind::mxf8f6f4, e2m1 in kind::mxf4
+  return (uint32_t)id << 4               // B's scale byte
+         | t << 7 | t << 10              // A and B type
+         | (uint32_t)(N >> 3) << 17      //
+         | 1u << 23                      // scales: e8m0
+         | (uint32_t)(M >> 7) << 27      //
+         | (uint32_t)id << 29;           // A's scale byte
+}
+
+template <MxFormat F, bool PAIR>
+__device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                          uint32_t sfb, uint32_t accumulate) {
+#define FH_MMA_MX(G, KIND)                                                              \
+  asm volatile(                                                                         \
+      "{\n\t.reg .pred p;\n\t"                                                          \
+      "setp.ne.b32 p, %6, 0;\n\t"                                                       \
+      "tcgen05.mma.cta_group::" G "." KIND " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), \
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                   \
+      : "memory")
+  if constexpr (F == MX_FP8) {
+    if constexpr (PAIR)
+      FH_MMA_MX("2", "kind::mxf8f6f4.block_scale.scale_vec::1X");
+    else
+      FH_MMA_MX("1", "kind::mxf8f6f4.block_scale.scale_vec::1X");
+  } else {
+    if constexpr (PAIR)
+      FH_MMA_MX("2", "kind::mxf4.block_scale.scale_vec::2X");
+    else
+      FH_MMA_MX("1", "kind::mxf4.block_scale.scale_vec::2X");
+  }
+#undef FH_MMA_MX
+}
+
+// Per-CTA TMA loads; in a pair the completion counts on the even CTA's barrier.
+template <bool PAIR>
+__device__ __forceinline__ void load_codes(const CUtensorMap* map, uint64_t* bar, void* dst, int c0, int c1) {
+  if constexpr (PAIR)
+    tma_load_2d_pair(map, mapa_shared(smem_u32(bar), 0), dst, c0, c1);
+  else
+    tma_load_2d(map, bar, dst, c0, c1);
+}
+template <bool PAIR>
+__device__ __forceinline__ void load_scales(const CUtensorMap* map, uint64_t* bar, void* dst, int kt, int rt) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(mapa_shared(smem_u32(bar), 0)), "r"(0), "r"(kt), "r"(rt)
+        : "memory");
+  else
+    tma_load_3d(map, bar, dst, 0, kt, rt);
+}
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (PAIR)
+    tc_commit_pair(bar, 0x3);
+  else
+    tc_commit(bar);
+}
+
+// The tanh form of GELU, x / (1 + e^(-2u)) with u = sqrt(2/pi) (x + 0.044715 x^3): the same
+// function as x (1 + tanh u) / 2. __expf is within a few 2^-22 relative here, far below the
+// rounding of every output type.
+__device__ __forceinline__ float gelu_sigmoid(float x) {
+  const float u2 = 1.5957691216057308f * fmaf(0.044715f * x, x * x, x);
+  return __fdividef(x, 1.f + __expf(-u2));
+}
+
+enum MxOut { MXO_F32 = 0, MXO_BF16 = 1, MXO_FP8 = 2, MXO_FP4 = 3 };
+
+struct MxParams {
+  const float* bias;  // or null
+  void* out;
+  uint8_t* oscales;  // of a microscaled output
+  int M, N, nk;      // nk: stages along K
+  int last;          // MMAs of the last stage
+  int num_m, ntiles;
+  int gelu;
+  int vec;  // rows of out are 16-byte aligned
+};
+
+// One row's 32 consecutive results: bias, activation.
+__device__ __forceinline__ void finish32(const MxParams& p, int col, float (&v)[32]) {
+  if (p.bias) {
+    if (col + 32 <= p.N) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 b = *reinterpret_cast<const float4*>(p.bias + col + j);
+        v[j] += b.x;
+        v[j + 1] += b.y;
+        v[j + 2] += b.z;
+        v[j + 3] += b.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (col + j < p.N) v[j] += p.bias[col + j];
+    }
+  }
+  if (p.gelu) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = gelu_sigmoid(v[j]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store32(const MxParams& p, int row, int col, const float (&v)[32]) {
+  T* dst = reinterpret_cast<T*>(p.out) + (long)row * p.N + col;
+  if (p.vec && col + 32 <= p.N) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) store8(dst + j, v + j);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (col + j < p.N) dst[j] = from_f<T>(v[j]);
+  }
+}
+
+// The block of 32 values as codes; returns its scale byte.
+template <MxFormat F>
+__device__ __forceinline__ uint32_t store_block(const MxParams& p, int row, int col, const float (&v)[32]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 32; j += 8) m = max(m, mx_amax8(v + j));
+  const uint32_t byte = mx_scale_byte<F>(m);
+  uint2 c[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c[j] = mx_encode8<F>(v + 8 * j, byte);
+  if (F == MX_FP8) {
+    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.out) + (long)row * p.N + col);
+    dst[0] = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
+    dst[1] = make_uint4(c[2].x, c[2].y, c[3].x, c[3].y);
+  } else {
+    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.out) + (long)row * (p.N / 2) + col / 2);
+    dst[0] = make_uint4(c[0].x, c[1].x, c[2].x, c[3].x);
+  }
+  return byte;
+}
+
+template <MxFormat F, int BN, bool PAIR, int OUT>
+__global__ void __launch_bounds__(MXG_THREADS, 1)
+    gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
+                   const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSW, MxParams p,
+                   unsigned* err) {
+  using S = MxShape<F, BN, PAIR>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::AUX_OFF);
+  uint64_t* empty = full + S::STAGES;
+  uint64_t* tfull = empty + S::STAGES;  // [2] accumulator complete
+  uint64_t* tempty = tfull + 2;         // [2] accumulator (its overlapped part at BN = 256) read
+  uint64_t* dealloc_bar = tempty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(dealloc_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const int cl = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  const int ncl = PAIR ? gridDim.x >> 1 : gridDim.x;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], EPI_THREADS * (PAIR ? 2 : 1));
+    }
+    mbar_init(dealloc_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmSA);
+    prefetch_tmap(&tmSW);
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_holder, S::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_holder, S::TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  if constexpr (PAIR)
+    cluster_sync_all();  // both CTAs' barriers are initialised before any cross-CTA signal
+  else
+    __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      pdl_wait();  // codes and scales may be the preceding kernel's output
+      int stage = 0;
+      uint32_t phase = 0;
+      int issues = 0;
+      for (int tile = cl; tile < p.ntiles; tile += ncl) {
+        const int m0 = (tile % p.num_m) * S::TM + (int)rank * 128;
+        const int n0 = (tile / p.num_m) * BN;
+        for (int kb = 0; kb < p.nk; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err, ERRBIT_TIMEOUT_GEMM)) goto producer_done;
+          uint8_t* sa = smem + stage * S::OPER_BYTES;
+          uint8_t* sf = smem + S::SF_OFF + stage * S::SF_BYTES;
+          if (rank == 0) mbar_expect_tx(&full[stage], S::TX_BYTES);
+          load_codes<PAIR>(&tmA, &full[stage], sa, kb * 128, m0);
+          load_codes<PAIR>(&tmW, &full[stage], sa + S::A_BYTES, kb * 128, n0 + (int)rank * S::WROWS);
+          load_scales<PAIR>(&tmSA, &full[stage], sf, kb * S::ATOMS, m0 >> 7);
+          load_scales<PAIR>(&tmSW, &full[stage], sf + S::SFA_BYTES, kb * S::ATOMS, n0 >> 7);
+          ++issues;
+          if (++stage == S::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    producer_done:
+      pdl_launch_dependents();
+      // tail: the MMA thread has released every stage filled last, so no arrival is in flight
+      // towards this CTA when it exits
+      if (!*abort_flag) {
+        for (int s = 0; s < S::STAGES && s < issues; ++s) {
+          int st = stage - 1 - s;
+          uint32_t ph = phase;
+          if (st < 0) {
+            st += S::STAGES;
+            ph ^= 1u;
+          }
+          mbar_wait(&empty[st], ph, abort_flag, err, ERRBIT_TIMEOUT_GEMM);
+        }
+      }
+      if (*abort_flag) {  // give copies already issued time to land
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 200000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int local = 0;
+      uint32_t it = 0;  // stages consumed
+      for (int tile = cl; tile < p.ntiles; tile += ncl, ++local) {
+        const int acc = local & 1;
+        // BN < 256: the accumulator's previous tile (local - 2) has been read. BN = 256: the part
+        // of the preceding tile's accumulator that this one overlaps has been read, by threads
+        // that had finished tile local - 2 before.
+        if (BN == 256) {
+          if (local >= 1 && !mbar_wait(&tempty[acc ^ 1], ((local - 1) >> 1) & 1, abort_flag, err, ERRBIT_TIMEOUT_GEMM))
+            break;
+        } else {
+          if (local >= 2 && !mbar_wait(&tempty[acc], ((local - 2) >> 1) & 1, abort_flag, err, ERRBIT_TIMEOUT_GEMM))
+            break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * S::ACC1;
+        // the tile's first W row within its scale row tile (BN = 64): 32 rows a column
+        const uint32_t sfb_off = BN < 128 ? (uint32_t)((((tile / p.num_m) * BN) & 127) >> 5) : 0u;
+        bool ok = true;
+        for (int kb = 0; kb < p.nk; ++kb, ++it) {
+          // the scale buffer is free once the MMAs of the stage NSF before this one are done
+          if (it >= S::NSF) {
+            const uint32_t u = it - S::NSF;
+            if (!mbar_wait(&empty[u % S::STAGES], (u / S::STAGES) & 1, abort_flag, err, ERRBIT_TIMEOUT_GEMM)) {
+              ok = false;
+              break;
+            }
+          }
+          if (!mbar_wait(&full[stage], phase, abort_flag, err, ERRBIT_TIMEOUT_GEMM)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sf_t = tmem_base + S::SF_COL + (it % S::NSF) * S::SF_COLS;
+          const uint32_t sf_s = smem_u32(smem + S::SF_OFF + stage * S::SF_BYTES);
+          // columns: A's tiles by K, then W's by (K, row tile); in shared memory W's lie by
+          // (row tile, K)
+#pragma unroll
+          for (int a = 0; a < S::ATOMS; ++a) {
+            tc_cp_scales<PAIR>(sf_t + 4 * a, sdesc_scales(sf_s + a * 512));
+#pragma unroll
+            for (int r = 0; r < S::SFBT; ++r)
+              tc_cp_scales<PAIR>(sf_t + S::SFA_COLS + 4 * (a * S::SFBT + r),
+                                 sdesc_scales(sf_s + S::SFA_BYTES + (r * S::ATOMS + a) * 512));
+          }
+          const uint32_t a_addr = smem_u32(smem + stage * S::OPER_BYTES);
+          const uint32_t b_addr = a_addr + S::A_BYTES;
+          // the last stage's MMAs end with K: its padding meets at most the second block of one
+          const int nmma = kb + 1 < p.nk ? 4 : p.last;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k >= nmma) break;
+            // 32 code bytes: 32 values (one block) of mxfp8, 64 values (two blocks) of mxfp4
+            const int atom = F == MX_FP8 ? 0 : k >> 1;
+            const int id = F == MX_FP8 ? k : 2 * (k & 1);
+            tc_mma_mx<F, PAIR>(d_tmem, sdesc_kmajor_sw128(a_addr + k * 32), sdesc_kmajor_sw128(b_addr + k * 32),
+                               idesc_mx(F, S::TM, BN, id), sf_t + 4 * atom,
+                               sf_t + S::SFA_COLS + 4 * S::SFBT * atom + sfb_off, (kb > 0 || k > 0) ? 1u : 0u);
+          }
+          commit<PAIR>(&empty[stage]);
+          if (++stage == S::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        commit<PAIR>(&tfull[acc]);
+      }
+      // tail: the epilogues have released the last accumulators (no arrival left in flight)
+      for (int i = 0; i < 2 && i < local; ++i) {
+        const int t = local - 1 - i;
+        if (!mbar_wait(&tempty[t & 1], (t >> 1) & 1, abort_flag, err, ERRBIT_TIMEOUT_GEMM)) break;
+      }
+    }
+  } else {
+    const int quarter = warp & 3;
+    const int sub = (warp - 2) >> 2;  // which half of the tile's columns
+    constexpr int HALF = BN / 2;
+    constexpr int NCH = HALF / 32;
+    const long okt = (p.N + 127) >> 7;
+    const int mpad = (p.M + 127) & ~127;
+    pdl_wait();
+    int local = 0;
+    for (int tile = cl; tile < p.ntiles; tile += ncl, ++local) {
+      const int acc = local & 1;
+      const int m0 = (tile % p.num_m) * S::TM + (int)rank * 128;
+      const int n0 = (tile / p.num_m) * BN + sub * HALF;
+      const int row = m0 + quarter * 32 + lane;
+      const bool ok = mbar_wait(&tfull[acc], (local >> 1) & 1, abort_flag, err, ERRBIT_TIMEOUT_GEMM);
+      if (!__all_sync(0xffffffffu, ok)) break;  // tcgen05.ld below is warp-collective
+      tc_fence_after();
+      const uint32_t tb = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * S::ACC1 + sub * HALF;
+      auto release = [&]() {
+        tc_fence_before();
+        if constexpr (PAIR)
+          mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+        else
+          mbar_arrive(&tempty[acc]);
+      };
+      // At BN = 256 the accumulators share columns 192-255: the last 64 of the first, the first
+      // 64 of the second. The warps that hold them read them first and release them, so that the
+      // next tile's MMAs run under the rest of this epilogue.
+      const bool holds = S::OVERLAP != 0 && sub == (acc ^ 1);
+      const int first = (S::OVERLAP != 0 && acc == 0) ? NCH / 2 : 0;  // chunk order: rotated for acc 0
+      if (S::OVERLAP != 0 && !holds) release();
+      uint32_t word = 0;
+      if (m0 + quarter * 32 < mpad) {
+#pragma unroll 1
+        for (int i = 0; i < NCH; ++i) {
+          const int ch = (i + first) & (NCH - 1);
+          const int col = n0 + ch * 32;
+          float v[32];
+          tmem_ld32(tb + ch * 32, v);
+          tc_wait_ld();
+          if (holds && i == NCH / 2 - 1) release();
+          if (col < p.N && row < p.M) {
+            finish32(p, col, v);
+            if constexpr (OUT == MXO_F32) store32<float>(p, row, col, v);
+            if constexpr (OUT == MXO_BF16) store32<bf16>(p, row, col, v);
+            if constexpr (OUT == MXO_FP8) word |= store_block<MX_FP8>(p, row, col, v) << (8 * ch);
+            if constexpr (OUT == MXO_FP4) word |= store_block<MX_FP4>(p, row, col, v) << (8 * ch);
+          }
+        }
+        if constexpr (OUT == MXO_FP8 || OUT == MXO_FP4) {
+          if ((n0 >> 7) < okt) {  // scales of this warp's columns; 0 beyond the tensor
+            uint8_t* dst = p.oscales + mx_scale_word(row, n0 >> 7, okt) + ((n0 >> 5) & 3);
+            if constexpr (NCH == 4) *reinterpret_cast<uint32_t*>(dst) = word;
+            if constexpr (NCH == 2) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)word;
+            if constexpr (NCH == 1) *dst = (uint8_t)word;
+          }
+        }
+      } else if (holds) {
+        release();
+      }
+      if (S::OVERLAP == 0) release();
+      if (*abort_flag) break;
+    }
+  }
+
+  // every role ends here with its warp converged again, so the barrier counts each warp once
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      // both CTAs are past their last TMEM access before the pair's allocation is released
+      if (lane == 0) {
+        mbar_arrive_cluster(mapa_shared(smem_u32(dealloc_bar), rank ^ 1u));
+        drain_wait(dealloc_bar, 0);
+      }
+      __syncwarp();
+      tc_fence_after();
+      tmem_dealloc_pair(tmem_base, S::TMEM_COLS);
+    } else {
+      tc_fence_after();
+      tmem_dealloc(tmem_base, S::TMEM_COLS);
+    }
+  }
+}
+
+template <MxFormat F, int BN, bool PAIR, int OUT>
+cudaError_t launch_mx(const MxMaps& maps, MxParams p, int K, int sms, cudaStream_t st) {
+  using S = MxShape<F, BN, PAIR>;
+  p.nk = (K + S::KB - 1) / S::KB;
+  p.last = (K - (p.nk - 1) * S::KB + S::KB / 4 - 1) / (S::KB / 4);
+  p.num_m = (p.M + S::TM - 1) / S::TM;
+  // a microscaled output's scale tiles are written whole: tiles up to the next multiple of 128
+  const int ncols = OUT >= MXO_FP8 ? (p.N + 127) / 128 * 128 : p.N;
+  const long tiles = (long)p.num_m * ((ncols + BN - 1) / BN);
+  if (tiles > 0x7fffffffL) return cudaErrorInvalidValue;
+  p.ntiles = (int)tiles;
+  const int slots = PAIR ? sms / 2 : sms;
+  const int grid = tiles < slots ? (int)tiles : slots;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(PAIR ? 2 * grid : grid);
+  cfg.blockDim = dim3(MXG_THREADS);
+  cfg.dynamicSmemBytes = S::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, gemm_mx_kernel<F, BN, PAIR, OUT>, maps.a, maps.w, maps.sa, maps.sw, p,
+                            (unsigned*)nullptr);
+}
+
+template <MxFormat F, int BN, bool PAIR, int OUT>
+cudaError_t prepare_one() {
+  return cudaFuncSetAttribute(gemm_mx_kernel<F, BN, PAIR, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)MxShape<F, BN, PAIR>::SMEM);
+}
+
+template <MxFormat F, int BN, bool PAIR>
+cudaError_t launch_out(const MxMaps& maps, const MxParams& p, int K, int out, int sms, cudaStream_t st) {
+  switch (out) {
+    case MXO_F32: return launch_mx<F, BN, PAIR, MXO_F32>(maps, p, K, sms, st);
+    case MXO_BF16: return launch_mx<F, BN, PAIR, MXO_BF16>(maps, p, K, sms, st);
+    case MXO_FP8: return launch_mx<F, BN, PAIR, MXO_FP8>(maps, p, K, sms, st);
+    default: return launch_mx<F, BN, PAIR, MXO_FP4>(maps, p, K, sms, st);
+  }
+}
+
+template <MxFormat F, int BN, bool PAIR>
+cudaError_t prepare_out() {
+  const cudaError_t es[] = {prepare_one<F, BN, PAIR, MXO_F32>(), prepare_one<F, BN, PAIR, MXO_BF16>(),
+                            prepare_one<F, BN, PAIR, MXO_FP8>(), prepare_one<F, BN, PAIR, MXO_FP4>()};
+  for (cudaError_t e : es)
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t gemm_mx_prepare() {
+  const cudaError_t es[] = {prepare_out<MX_FP8, 128, false>(), prepare_out<MX_FP4, 128, false>()};
+  for (cudaError_t e : es)
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
+}
+
+MxTile gemm_mx_tile(int M, int N, int K, int sms) {
+  (void)M;
+  (void)N;
+  (void)K;
+  (void)sms;
+  return MxTile{128, false};
+}
+
+cudaError_t gemm_mx(const MxMaps& maps, MxTile t, const float* bias, void* out, void* oscales, int M, int N, int K,
+                    int fmt, bool gelu, int out_kind, int sms, cudaStream_t st) {
+  MxParams p = {};
+  p.bias = bias;
+  p.out = out;
+  p.oscales = (uint8_t*)oscales;
+  p.M = M;
+  p.N = N;
+  p.gelu = gelu;
+  p.vec = ((long)N * (out_kind == MXO_F32 ? 4 : 2)) % 16 == 0;
+  return fmt == MX_FP8 ? launch_out<MX_FP8, 128, false>(maps, p, K, out_kind, sms, st)
+                       : launch_out<MX_FP4, 128, false>(maps, p, K, out_kind, sms, st);
+}
+
+}  // namespace fh

@@ -131,4 +131,29 @@ template <typename WT>
 cudaError_t audio_linear(const WT* W, const float* x, const float* bias, float* part, float* y, int N, int K, int R,
                          int relu, int per, int ostride, int ooff, cudaStream_t st);
 
+// Microscaled operators (mx.cu, gemm_mx.cu; the format: mx.cuh). `fmt` 0: mxfp8, 1: mxfp4;
+// `out_kind` 0: float32, 1: bfloat16, 2: mxfp8, 3: mxfp4. K and D are multiples of 32.
+cudaError_t mx_quantize(const void* x, long ldx, int M, int K, bool x_bf16, int fmt, void* data, void* scales,
+                        cudaStream_t st);
+cudaError_t mx_dequantize(const void* data, const void* scales, int M, int K, int fmt, void* out, bool out_bf16,
+                          cudaStream_t st);
+// sum = x + res (x's type), out = sum / rms(sum) * a, or * (1 + a) + c where c is not null; row r
+// takes the vectors at a, c + (r / rows_per_batch) * bstride. D <= 16384.
+cudaError_t add_rms_norm(const void* x, bool x_bf16, const void* res, bool res_bf16, void* sum, const float* a,
+                         const float* c, long bstride, int rows_per_batch, int M, int D, float eps, int out_kind,
+                         void* out, void* scales, cudaStream_t st);
+// The product's TMA maps: codes as bytes (box 128 x rows, 128-byte swizzle) and scale tiles as
+// [row tiles][K tiles][128 words] (box 128 words x tiles per stage x row tiles).
+struct MxMaps {
+  CUtensorMap a, w, sa, sw;
+};
+struct MxTile {
+  int bn;     // columns of a tile
+  bool pair;  // 256-row tiles on CTA pairs, each loading half of the tile's W rows
+};
+cudaError_t gemm_mx_prepare();
+MxTile gemm_mx_tile(int M, int N, int K, int sms);
+cudaError_t gemm_mx(const MxMaps& maps, MxTile t, const float* bias, void* out, void* oscales, int M, int N, int K,
+                    int fmt, bool gelu, int out_kind, int sms, cudaStream_t st);
+
 }  // namespace fh

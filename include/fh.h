@@ -65,7 +65,12 @@ enum fh_status {
   FH_ERR_UNSUPPORTED = -6   /* device is not sm_100, or dtype/shape not supported */
 };
 
-enum fh_dtype { FH_F32 = 0, FH_BF16 = 1 };
+enum fh_dtype {
+  FH_F32 = 0,
+  FH_BF16 = 1,
+  FH_MXFP8 = 2, /* microscaled e4m3 and e2m1 (fh_ops.h): operators only, not a model's type */
+  FH_MXFP4 = 3
+};
 
 /* Model configuration. The Lite network is {1536, 12, 128, 8960, 30, 128, 5, 16,
  * 16, 32, max_batch, FH_BF16, 1e4, {44, 42, 42}, 1e-6, device}. Constraints:

@@ -3,6 +3,21 @@
  * parity tests of single kernels. Same conventions as fh.h (return codes,
  * fh_last_error, caller-owned 16-byte-aligned device pointers, asynchronous on
  * `stream`). They allocate nothing.
+ *
+ * Microscaled tensors (types FH_MXFP8 and FH_MXFP4) of M rows x K columns, K % 32 == 0, hold a
+ * number as an element times its block's scale; a block is 32 consecutive values of a row.
+ *   data    FH_MXFP8: e4m3 (largest value 448), one byte each, row-major [M][K]
+ *           FH_MXFP4: e2m1 (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives), two to a byte, the
+ *           even column in the low four bits, row-major [M][K / 2]
+ *   scales  e8m0, one byte per block: 2^(byte - 127), 255 is NaN. In tiles of 128 rows x 4
+ *           blocks: row r, block k at ((r / 128) * ceil(K / 128) + k / 4) * 512 + (r % 32) * 16 +
+ *           ((r % 128) / 32) * 4 + k % 4 (the order in which the tensor core takes them);
+ *           fh_mx_scale_bytes(M, K) bytes, those past the tensor 0
+ * Every operator that writes one chooses each block's scale as the smallest power of two,
+ * 2^-127 or more, under which the block's largest magnitude is an element, and rounds each
+ * value / scale to the nearest element, ties to the even code. A block with an infinity or a
+ * NaN gets the scale byte 255 and zero codes: all its values read back as NaN.
+ * M <= 2^27, K and N <= 2^20.
  */
 #ifndef FH_OPS_H_
 #define FH_OPS_H_
@@ -60,6 +75,43 @@ int fh_op_cross_attention(const void* q, const float* ssq_q, const void* kv, con
  * LayerNorm with the biased variance, no gain of its own; eps inside the root. */
 int fh_op_row_norm(const float* x, void* out, int M, int D, int mode, const float* a, const float* c, long bstride,
                    int rows_per_batch, float eps, int dtype, void* stream);
+
+/* Bytes of a microscaled tensor's two parts; 0 for a type or a size that has none. */
+size_t fh_mx_data_bytes(int M, int K, int mxtype);
+size_t fh_mx_scale_bytes(int M, int K);
+
+/* x [M][K] in dtype (FH_F32 or FH_BF16), rows ldx elements apart (ldx >= K, a multiple of 16
+ * bytes), to the microscaled type mxtype. Errors: FH_ERR_ARG (pointers, types), FH_ERR_SHAPE. */
+int fh_op_quantize(const void* x, long ldx, int M, int K, int dtype, int mxtype, void* data, void* scales,
+                   void* stream);
+
+/* The values of a microscaled tensor, out [M][K] in dtype: exact, but that values of 2^128 and
+ * above (which scales of 2^118 and more can make) become infinite, and that FH_BF16 rounds
+ * what is no multiple of 2^-133. */
+int fh_op_dequantize(const void* data, const void* scales, int M, int K, int mxtype, void* out, int dtype,
+                     void* stream);
+
+/* The residual's addition and the RMS norm after it, with the result in the type that the next
+ * Linear takes: sum = x + res in x's type, and with n = sum / sqrt(mean(sum^2) + eps) per row (of
+ * the sum as it is kept), out = n * a where c is null, n * (1 + a) + c elsewhere. x, sum [M][D] in
+ * x_dtype, res [M][D] in res_dtype (FH_F32 or FH_BF16); D % 32 == 0, D <= 16384; a, c float32
+ * vectors of D, row r's at a + (r / rows_per_batch) * bstride (bstride % 4 == 0). out_type any
+ * of fh_dtype; out_scales for the microscaled ones, else null. sum may be x, or res where its
+ * type is x's; it may not overlap them otherwise, nor out anything. */
+int fh_op_add_rms_norm(const void* x, int x_dtype, const void* res, int res_dtype, void* sum, const float* a,
+                       const float* c, long bstride, int rows_per_batch, int M, int D, float eps, int out_type,
+                       void* out, void* out_scales, void* stream);
+
+enum fh_act { FH_ACT_NONE = 0, FH_ACT_GELU = 1 };
+
+/* out [M][N] = act(A [M][K] * W [N][K]^T + bias [N]) of two microscaled operands of one type, on
+ * the block-scaled tensor core, accumulated in fp32; bias float32 or null; act FH_ACT_GELU: the
+ * tanh form of GELU. K % 32 == 0; N any, but a multiple of 32 for a microscaled out. out_type any
+ * of fh_dtype; out_scales for the microscaled ones, else null. A row or column with a NaN scale
+ * gives NaN results. out may not overlap the operands. */
+int fh_op_linear_mx(const void* A, const void* A_scales, const void* W, const void* W_scales, const float* bias,
+                    int M, int N, int K, int mxtype, int act, int out_type, void* out, void* out_scales,
+                    void* stream);
 
 /* Failure-detection check (no counterpart on the pages; reading of the pages'
  * reject-don't-hang stance): launches one CTA whose mbarrier wait has no arriving
