@@ -114,18 +114,33 @@ bool make_qkv_map(CUtensorMap* map, const void* base, uint64_t L, uint64_t plane
 // [128], box 128 x box_kt x box_rt. What a box reads past either end is zero.
 bool make_mx_maps(CUtensorMap* codes, CUtensorMap* scales, const void* data, const void* sc, uint64_t rows,
                   uint64_t pitch, uint64_t K, uint32_t box_rows, uint32_t box_kt, uint32_t box_rt) {
-  cuuint64_t dims[2] = {pitch, rows};
+  cuuint64_t dims[2] = {pitch / 4, rows};
   cuuint64_t strides[1] = {pitch};
-  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t box[2] = {32, box_rows};
   cuuint64_t sdims[3] = {128, (K + 127) / 128, (rows + 127) / 128};
   cuuint64_t sstrides[2] = {512, 512 * sdims[1]};
   cuuint32_t sbox[3] = {128, box_kt, box_rt};
   cuuint32_t estr[3] = {1, 1, 1};
-  return g_encode(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(data), dims, strides, box, estr,
+  return g_encode(codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(data), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
          g_encode(scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(sc), sdims, sstrides, sbox, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Output [rows] of `row_bytes` each as 32-bit words, box box_bytes x 32 rows with its own width's swizzle.
+bool make_mx_out_map(CUtensorMap* map, void* out, uint64_t rows, uint64_t row_bytes, uint32_t box_bytes) {
+  cuuint64_t dims[2] = {row_bytes / 4, rows};
+  cuuint64_t strides[1] = {row_bytes};
+  cuuint32_t box[2] = {box_bytes / 4, 32};
+  cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapSwizzle sw = box_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                : box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                : box_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                                  : CU_TENSOR_MAP_SWIZZLE_NONE;
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, out, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1442,6 +1457,10 @@ int fh_op_linear_mx(const void* A, const void* A_scales, const void* W, const vo
   const uint64_t pitch = mxtype == FH_MXFP4 ? K / 2 : K;
   const uint32_t kt = mxtype == FH_MXFP4 ? 2 : 1;
   MxMaps maps;
+  memset(&maps.o, 0, sizeof maps.o);
+  const uint64_t orow = (uint64_t)N * (out_type == FH_F32 ? 8 : out_type == FH_BF16 ? 4 : out_type == FH_MXFP8 ? 2 : 1) / 2;
+  if (gemm_mx_tma_out(N, out_type) && !make_mx_out_map(&maps.o, out, M, orow, gemm_mx_out_row_bytes(t, out_type)))
+    return fail(FH_ERR_CUDA, "tensor map encoding");
   if (!make_mx_maps(&maps.a, &maps.sa, A, A_scales, M, pitch, K, 128, kt, 1) ||
       !make_mx_maps(&maps.w, &maps.sw, W, W_scales, N, pitch, K, t.pair ? t.bn / 2 : t.bn, kt, (t.bn + 127) / 128))
     return fail(FH_ERR_CUDA, "tensor map encoding");

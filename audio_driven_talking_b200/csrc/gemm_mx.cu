@@ -26,6 +26,18 @@ namespace {
 
 constexpr int MXG_THREADS = 320;
 constexpr int EPI_THREADS = 256;
+constexpr uint32_t BOX_BYTES = 4096;  // of an epilogue warp: 32 rows of up to 128 bytes
+
+enum MxOut { MXO_F32 = 0, MXO_BF16 = 1, MXO_FP8 = 2, MXO_FP4 = 3 };
+
+// Columns of a warp's staging box: 128 bytes of a row, as far as its share of the tile, `half`
+// columns, divides into boxes; a microscaled output's box is the whole share, in 32s if that is 96.
+constexpr int box_cols(int out, int half) {
+  return out == MXO_F32 ? 32 : out == MXO_BF16 ? (half % 64 == 0 ? 64 : 32) : half % 64 == 0 ? half : 32;
+}
+constexpr int box_row_bytes(int out, int half) {
+  return box_cols(out, half) * (out == MXO_F32 ? 8 : out == MXO_BF16 ? 4 : out == MXO_FP8 ? 2 : 1) / 2;
+}
 
 template <MxFormat F, int BN, bool PAIR>
 struct MxShape {
@@ -42,11 +54,13 @@ struct MxShape {
   static constexpr uint32_t SF_BYTES = SFA_BYTES + SFB_BYTES;
   static constexpr uint32_t STAGE_BYTES = OPER_BYTES + SF_BYTES;
   static constexpr uint32_t TX_BYTES = STAGE_BYTES * (PAIR ? 2 : 1);
+  static constexpr uint32_t OUT_BYTES = 8 * BOX_BYTES;  // the epilogue warps' staging boxes
   static constexpr uint32_t AUX_BYTES = 1024;
-  static constexpr int FIT = (int)((227u * 1024u - 1024u - AUX_BYTES) / STAGE_BYTES);
+  static constexpr int FIT = (int)((227u * 1024u - 1024u - AUX_BYTES - OUT_BYTES) / STAGE_BYTES);
   static constexpr int STAGES = FIT < 8 ? FIT : 8;
-  static constexpr uint32_t SF_OFF = STAGES * OPER_BYTES;
-  static constexpr uint32_t AUX_OFF = STAGES * STAGE_BYTES;
+  static constexpr uint32_t OUT_OFF = STAGES * OPER_BYTES;
+  static constexpr uint32_t SF_OFF = OUT_OFF + OUT_BYTES;
+  static constexpr uint32_t AUX_OFF = SF_OFF + STAGES * SF_BYTES;
   static constexpr uint32_t SMEM = AUX_OFF + AUX_BYTES + 1024;
   // TMEM columns: two accumulators (at BN = 256 the second starts inside the first: see the
   // epilogue), then the scale buffers
@@ -55,9 +69,10 @@ struct MxShape {
   static constexpr int SF_COL = ACC1 + BN;
   static constexpr int SFA_COLS = 4 * ATOMS;
   static constexpr int SF_COLS = SFA_COLS + 4 * ATOMS * SFBT;
-  static constexpr int NSF = 2;
+  static constexpr int NSF_FIT = (512 - SF_COL) / SF_COLS;
+  static constexpr int NSF = NSF_FIT < 4 ? NSF_FIT : 4;  // scale buffers
   static constexpr uint32_t TMEM_COLS = 512;
-  static_assert(SF_COL + NSF * SF_COLS <= 512, "TMEM");
+  static_assert(NSF >= 2 && SF_COL + NSF * SF_COLS <= 512, "TMEM");
   static_assert(STAGES > NSF, "a scale buffer's stage is still in the ring when it is reused");
 };
 
@@ -146,8 +161,6 @@ __device__ __forceinline__ float gelu_sigmoid(float x) {
   return __fdividef(x, 1.f + __expf(-u2));
 }
 
-enum MxOut { MXO_F32 = 0, MXO_BF16 = 1, MXO_FP8 = 2, MXO_FP4 = 3 };
-
 struct MxParams {
   const float* bias;  // or null
   void* out;
@@ -156,7 +169,7 @@ struct MxParams {
   int last;          // MMAs of the last stage
   int num_m, ntiles;
   int gelu;
-  int vec;  // rows of out are 16-byte aligned
+  int tma;  // rows of out are 16-byte aligned: boxes leave by TMA
 };
 
 // One row's 32 consecutive results: bias, activation.
@@ -183,45 +196,116 @@ __device__ __forceinline__ void finish32(const MxParams& p, int col, float (&v)[
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void store32(const MxParams& p, int row, int col, const float (&v)[32]) {
-  T* dst = reinterpret_cast<T*>(p.out) + (long)row * p.N + col;
-  if (p.vec && col + 32 <= p.N) {
+// 16 bytes, unit `j` of a row of RB bytes, into a staging box as the TMA swizzle of that width has it
+template <int RB>
+__device__ __forceinline__ uint4* box_unit(uint8_t* box, int row, int j) {
+  const int x = RB == 128 ? j ^ (row & 7) : RB == 64 ? j ^ ((row >> 1) & 3) : RB == 32 ? j ^ ((row >> 2) & 1) : j;
+  return reinterpret_cast<uint4*>(box + row * RB + x * 16);
+}
+
+// One row's 32 consecutive results into the warp's box, `c0` columns from its left; the block's
+// scale byte for microscaled ones.
+template <int OUT, int RB>
+__device__ __forceinline__ uint32_t stage32(uint8_t* box, int row, int c0, const float (&v)[32]) {
+  if constexpr (OUT == MXO_F32) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 8) store8(dst + j, v + j);
+    for (int j = 0; j < 8; ++j)
+      *reinterpret_cast<float4*>(box_unit<RB>(box, row, c0 / 4 + j)) =
+          make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    return 0;
+  } else if constexpr (OUT == MXO_BF16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) store8(reinterpret_cast<bf16*>(box_unit<RB>(box, row, c0 / 8 + j)), v + 8 * j);
+    return 0;
   } else {
+    constexpr MxFormat F = OUT == MXO_FP8 ? MX_FP8 : MX_FP4;
+    uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (col + j < p.N) dst[j] = from_f<T>(v[j]);
+    for (int j = 0; j < 32; j += 8) m = max(m, mx_amax8(v + j));
+    const uint32_t byte = mx_scale_byte<F>(m);
+    uint2 c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = mx_encode8<F>(v + 8 * j, byte);
+    if constexpr (F == MX_FP8) {
+      *box_unit<RB>(box, row, c0 / 16) = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
+      *box_unit<RB>(box, row, c0 / 16 + 1) = make_uint4(c[2].x, c[2].y, c[3].x, c[3].y);
+    } else {
+      *box_unit<RB>(box, row, c0 / 32) = make_uint4(c[0].x, c[1].x, c[2].x, c[3].x);
+    }
+    return byte;
   }
 }
 
-// The block of 32 values as codes; returns its scale byte.
-template <MxFormat F>
-__device__ __forceinline__ uint32_t store_block(const MxParams& p, int row, int col, const float (&v)[32]) {
-  uint32_t m = 0;
+// A box's columns col .. col + COLS of rows row0 .. row0 + 32 to rows that are not 16-byte aligned:
+// consecutive lanes take consecutive columns.
+template <int OUT, int RB, int COLS>
+__device__ __forceinline__ void copy_box(const MxParams& p, uint8_t* box, int row0, int col, int lane) {
+  using T = typename std::conditional<OUT == MXO_F32, float, bf16>::type;
+  constexpr int PER = 16 / (int)sizeof(T);
+  const int rows = min(32, p.M - row0);
+  for (int r = 0; r < rows; ++r) {
+    T* dst = reinterpret_cast<T*>(p.out) + (long)(row0 + r) * p.N + col;
 #pragma unroll
-  for (int j = 0; j < 32; j += 8) m = max(m, mx_amax8(v + j));
-  const uint32_t byte = mx_scale_byte<F>(m);
-  uint2 c[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) c[j] = mx_encode8<F>(v + 8 * j, byte);
-  if (F == MX_FP8) {
-    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.out) + (long)row * p.N + col);
-    dst[0] = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
-    dst[1] = make_uint4(c[2].x, c[2].y, c[3].x, c[3].y);
-  } else {
-    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.out) + (long)row * (p.N / 2) + col / 2);
-    dst[0] = make_uint4(c[0].x, c[1].x, c[2].x, c[3].x);
+    for (int c = 0; c < COLS; c += 32)
+      if (col + c + lane < p.N)
+        dst[c + lane] = reinterpret_cast<const T*>(box_unit<RB>(box, r, (c + lane) / PER))[(c + lane) % PER];
   }
-  return byte;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// mbar_wait (common.cuh: bounded, false on giving up) by a whole warp, with one answer
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || mbar_wait(bar, parity, abort, err, ERRBIT_TIMEOUT_GEMM));
+}
+
+// A place in a ring of N barriers
+template <int N>
+struct Ring {
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// The scale copies and the MMAs (NMMA of 4) of one stage; `ad`, `bd`, `sd` describe its operands
+// and its scale tiles in shared memory, `sf` its scale buffer in TMEM.
+template <MxFormat F, int BN, bool PAIR>
+__device__ __forceinline__ void issue_scales(uint64_t sd, uint32_t sf) {
+  using S = MxShape<F, BN, PAIR>;
+  // columns: A's tiles by K, then W's by (K, row tile); in shared memory W's lie by (row tile, K)
+#pragma unroll
+  for (int a = 0; a < S::ATOMS; ++a) {
+    tc_cp_scales<PAIR>(sf + 4 * a, sd + a * 32);
+#pragma unroll
+    for (int r = 0; r < S::SFBT; ++r)
+      tc_cp_scales<PAIR>(sf + S::SFA_COLS + 4 * (a * S::SFBT + r), sd + (S::ATOMS + r * S::ATOMS + a) * 32);
+  }
+}
+template <MxFormat F, int BN, bool PAIR>
+__device__ __forceinline__ void issue_mma(int k, uint32_t d, uint64_t ad, uint64_t bd, uint32_t sf, uint32_t sfb_off,
+                                          uint32_t accumulate) {
+  using S = MxShape<F, BN, PAIR>;
+  // 32 code bytes: 32 values (one block) of mxfp8, 64 values (two blocks) of mxfp4
+  const int atom = F == MX_FP8 ? 0 : k >> 1;
+  const int id = F == MX_FP8 ? k : 2 * (k & 1);
+  tc_mma_mx<F, PAIR>(d, ad + 2 * k, bd + 2 * k, idesc_mx(F, S::TM, BN, id), sf + 4 * atom,
+                     sf + S::SFA_COLS + 4 * S::SFBT * atom + sfb_off, accumulate);
 }
 
 template <MxFormat F, int BN, bool PAIR, int OUT>
 __global__ void __launch_bounds__(MXG_THREADS, 1)
     gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
-                   const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSW, MxParams p,
-                   unsigned* err) {
+                   const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSW,
+                   const __grid_constant__ CUtensorMap tmO, MxParams p, unsigned* err) {
   using S = MxShape<F, BN, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -233,7 +317,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(dealloc_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
   const int cl = PAIR ? blockIdx.x >> 1 : blockIdx.x;
@@ -255,6 +339,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
     prefetch_tmap(&tmW);
     prefetch_tmap(&tmSA);
     prefetch_tmap(&tmSW);
+    if (OUT >= MXO_FP8 || p.tma) prefetch_tmap(&tmO);
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -275,145 +360,127 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
   const uint32_t tmem_base = *tmem_holder;
 
   if (warp == 0) {
-    if (lane == 0) {
-      pdl_wait();  // codes and scales may be the preceding kernel's output
-      int stage = 0;
-      uint32_t phase = 0;
-      int issues = 0;
-      for (int tile = cl; tile < p.ntiles; tile += ncl) {
-        const int m0 = (tile % p.num_m) * S::TM + (int)rank * 128;
-        const int n0 = (tile / p.num_m) * BN;
-        for (int kb = 0; kb < p.nk; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err, ERRBIT_TIMEOUT_GEMM)) goto producer_done;
-          uint8_t* sa = smem + stage * S::OPER_BYTES;
-          uint8_t* sf = smem + S::SF_OFF + stage * S::SF_BYTES;
-          if (rank == 0) mbar_expect_tx(&full[stage], S::TX_BYTES);
-          load_codes<PAIR>(&tmA, &full[stage], sa, kb * 128, m0);
-          load_codes<PAIR>(&tmW, &full[stage], sa + S::A_BYTES, kb * 128, n0 + (int)rank * S::WROWS);
-          load_scales<PAIR>(&tmSA, &full[stage], sf, kb * S::ATOMS, m0 >> 7);
-          load_scales<PAIR>(&tmSW, &full[stage], sf + S::SFA_BYTES, kb * S::ATOMS, n0 >> 7);
-          ++issues;
-          if (++stage == S::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+    pdl_wait();  // codes and scales may be the preceding kernel's output
+    Ring<S::STAGES> cur;
+    int issues = 0;
+    bool ok = true;
+    for (int tile = cl; ok && tile < p.ntiles; tile += ncl) {
+      const int m0 = (tile % p.num_m) * S::TM + (int)rank * 128;
+      const int n0 = (tile / p.num_m) * BN;
+      for (int kb = 0; kb < p.nk; ++kb) {
+        if (!warp_wait(&empty[cur.i], cur.phase ^ 1u, abort_flag, err)) {
+          ok = false;
+          break;
         }
+        if (elect_one()) {
+          uint8_t* sa = smem + cur.i * S::OPER_BYTES;
+          uint8_t* sf = smem + S::SF_OFF + cur.i * S::SF_BYTES;
+          if (rank == 0) mbar_expect_tx(&full[cur.i], S::TX_BYTES);
+          load_codes<PAIR>(&tmA, &full[cur.i], sa, kb * 32, m0);
+          load_codes<PAIR>(&tmW, &full[cur.i], sa + S::A_BYTES, kb * 32, n0 + (int)rank * S::WROWS);
+          load_scales<PAIR>(&tmSA, &full[cur.i], sf, kb * S::ATOMS, m0 >> 7);
+          load_scales<PAIR>(&tmSW, &full[cur.i], sf + S::SFA_BYTES, kb * S::ATOMS, n0 >> 7);
+        }
+        __syncwarp();
+        ++issues;
+        cur.next();
       }
-    producer_done:
-      pdl_launch_dependents();
-      // tail: the MMA thread has released every stage filled last, so no arrival is in flight
-      // towards this CTA when it exits
-      if (!*abort_flag) {
-        for (int s = 0; s < S::STAGES && s < issues; ++s) {
-          int st = stage - 1 - s;
-          uint32_t ph = phase;
-          if (st < 0) {
-            st += S::STAGES;
-            ph ^= 1u;
-          }
-          mbar_wait(&empty[st], ph, abort_flag, err, ERRBIT_TIMEOUT_GEMM);
-        }
+    }
+    pdl_launch_dependents();
+    // tail: the MMA thread has released every stage filled last, so no arrival is in flight
+    // towards this CTA when it exits
+    for (int s = 0; ok && s < S::STAGES && s < issues; ++s) {
+      int st = cur.i - 1 - s;
+      uint32_t ph = cur.phase;
+      if (st < 0) {
+        st += S::STAGES;
+        ph ^= 1u;
       }
-      if (*abort_flag) {  // give copies already issued time to land
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 200000ull) {
-        }
+      ok = warp_wait(&empty[st], ph, abort_flag, err);
+    }
+    if (!ok) {  // give copies already issued time to land
+      const uint64_t t0 = globaltimer();
+      while (globaltimer() - t0 < 200000ull) {
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int local = 0;
-      uint32_t it = 0;  // stages consumed
+    if (rank == 0) {
+      Ring<S::STAGES> cur, done;  // the stage to issue, and the one whose MMAs free its scale buffer
+      int sfi = 0, local = 0;
+      int pending = 0;  // stages issued, up to NSF
+      const uint64_t ad0 = sdesc_kmajor_sw128(smem_u32(smem));
+      const uint64_t bd0 = sdesc_kmajor_sw128(smem_u32(smem) + S::A_BYTES);
+      const uint64_t sd0 = sdesc_scales(smem_u32(smem) + S::SF_OFF);
+      bool ok = true;
       for (int tile = cl; tile < p.ntiles; tile += ncl, ++local) {
         const int acc = local & 1;
         // BN < 256: the accumulator's previous tile (local - 2) has been read. BN = 256: the part
         // of the preceding tile's accumulator that this one overlaps has been read, by threads
         // that had finished tile local - 2 before.
         if (BN == 256) {
-          if (local >= 1 && !mbar_wait(&tempty[acc ^ 1], ((local - 1) >> 1) & 1, abort_flag, err, ERRBIT_TIMEOUT_GEMM))
-            break;
+          if (local >= 1 && !warp_wait(&tempty[acc ^ 1], ((local - 1) >> 1) & 1, abort_flag, err)) break;
         } else {
-          if (local >= 2 && !mbar_wait(&tempty[acc], ((local - 2) >> 1) & 1, abort_flag, err, ERRBIT_TIMEOUT_GEMM))
-            break;
+          if (local >= 2 && !warp_wait(&tempty[acc], ((local - 2) >> 1) & 1, abort_flag, err)) break;
         }
-        tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * S::ACC1;
-        // the tile's first W row within its scale row tile (BN = 64): 32 rows a column
-        const uint32_t sfb_off = BN < 128 ? (uint32_t)((((tile / p.num_m) * BN) & 127) >> 5) : 0u;
-        bool ok = true;
-        for (int kb = 0; kb < p.nk; ++kb, ++it) {
+        // the tile's first W row within its scale row tile (BN = 64, 192): 32 rows a column
+        const uint32_t sfb_off = BN % 128 != 0 ? (uint32_t)((((tile / p.num_m) * BN) & 127) >> 5) : 0u;
+        for (int kb = 0; kb < p.nk; ++kb) {
           // the scale buffer is free once the MMAs of the stage NSF before this one are done
-          if (it >= S::NSF) {
-            const uint32_t u = it - S::NSF;
-            if (!mbar_wait(&empty[u % S::STAGES], (u / S::STAGES) & 1, abort_flag, err, ERRBIT_TIMEOUT_GEMM)) {
-              ok = false;
-              break;
-            }
+          if (pending == S::NSF) {
+            ok = warp_wait(&empty[done.i], done.phase, abort_flag, err);
+            done.next();
+          } else {
+            ++pending;
           }
-          if (!mbar_wait(&full[stage], phase, abort_flag, err, ERRBIT_TIMEOUT_GEMM)) {
-            ok = false;
-            break;
-          }
+          ok = ok && warp_wait(&full[cur.i], cur.phase, abort_flag, err);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sf_t = tmem_base + S::SF_COL + (it % S::NSF) * S::SF_COLS;
-          const uint32_t sf_s = smem_u32(smem + S::SF_OFF + stage * S::SF_BYTES);
-          // columns: A's tiles by K, then W's by (K, row tile); in shared memory W's lie by
-          // (row tile, K)
+          if (elect_one()) {
+            const uint32_t sf = tmem_base + S::SF_COL + sfi * S::SF_COLS;
+            const uint64_t ad = ad0 + cur.i * (S::OPER_BYTES >> 4), bd = bd0 + cur.i * (S::OPER_BYTES >> 4);
+            issue_scales<F, BN, PAIR>(sd0 + cur.i * (S::SF_BYTES >> 4), sf);
+            issue_mma<F, BN, PAIR>(0, d_tmem, ad, bd, sf, sfb_off, kb > 0);
+            if (kb + 1 < p.nk || p.last == 4) {
 #pragma unroll
-          for (int a = 0; a < S::ATOMS; ++a) {
-            tc_cp_scales<PAIR>(sf_t + 4 * a, sdesc_scales(sf_s + a * 512));
-#pragma unroll
-            for (int r = 0; r < S::SFBT; ++r)
-              tc_cp_scales<PAIR>(sf_t + S::SFA_COLS + 4 * (a * S::SFBT + r),
-                                 sdesc_scales(sf_s + S::SFA_BYTES + (r * S::ATOMS + a) * 512));
+              for (int k = 1; k < 4; ++k) issue_mma<F, BN, PAIR>(k, d_tmem, ad, bd, sf, sfb_off, 1u);
+            } else {  // the last MMAs end with K: its padding meets at most the second block of one
+              if (p.last > 1) issue_mma<F, BN, PAIR>(1, d_tmem, ad, bd, sf, sfb_off, 1u);
+              if (p.last > 2) issue_mma<F, BN, PAIR>(2, d_tmem, ad, bd, sf, sfb_off, 1u);
+            }
+            commit<PAIR>(&empty[cur.i]);
+            if (kb + 1 == p.nk) commit<PAIR>(&tfull[acc]);
           }
-          const uint32_t a_addr = smem_u32(smem + stage * S::OPER_BYTES);
-          const uint32_t b_addr = a_addr + S::A_BYTES;
-          // the last stage's MMAs end with K: its padding meets at most the second block of one
-          const int nmma = kb + 1 < p.nk ? 4 : p.last;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k >= nmma) break;
-            // 32 code bytes: 32 values (one block) of mxfp8, 64 values (two blocks) of mxfp4
-            const int atom = F == MX_FP8 ? 0 : k >> 1;
-            const int id = F == MX_FP8 ? k : 2 * (k & 1);
-            tc_mma_mx<F, PAIR>(d_tmem, sdesc_kmajor_sw128(a_addr + k * 32), sdesc_kmajor_sw128(b_addr + k * 32),
-                               idesc_mx(F, S::TM, BN, id), sf_t + 4 * atom,
-                               sf_t + S::SFA_COLS + 4 * S::SFBT * atom + sfb_off, (kb > 0 || k > 0) ? 1u : 0u);
-          }
-          commit<PAIR>(&empty[stage]);
-          if (++stage == S::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          __syncwarp();
+          cur.next();
+          if (++sfi == S::NSF) sfi = 0;
         }
         if (!ok) break;
-        commit<PAIR>(&tfull[acc]);
       }
       // tail: the epilogues have released the last accumulators (no arrival left in flight)
       for (int i = 0; i < 2 && i < local; ++i) {
         const int t = local - 1 - i;
-        if (!mbar_wait(&tempty[t & 1], (t >> 1) & 1, abort_flag, err, ERRBIT_TIMEOUT_GEMM)) break;
+        if (!warp_wait(&tempty[t & 1], (t >> 1) & 1, abort_flag, err)) break;
       }
     }
   } else {
     const int quarter = warp & 3;
     const int sub = (warp - 2) >> 2;  // which half of the tile's columns
     constexpr int HALF = BN / 2;
-    constexpr int NCH = HALF / 32;
+    constexpr int NCH = HALF / 32;              // chunks of 32 columns
+    constexpr int PER = NCH % 2 == 0 ? 2 : 1;   // chunks read from TMEM at once
+    constexpr int COLS = box_cols(OUT, HALF), RB = box_row_bytes(OUT, HALF), GROUP = COLS / 32;
     const long okt = (p.N + 127) >> 7;
     const int mpad = (p.M + 127) & ~127;
+    uint8_t* box = smem + S::OUT_OFF + (warp - 2) * BOX_BYTES;
     pdl_wait();
     int local = 0;
     for (int tile = cl; tile < p.ntiles; tile += ncl, ++local) {
       const int acc = local & 1;
       const int m0 = (tile % p.num_m) * S::TM + (int)rank * 128;
       const int n0 = (tile / p.num_m) * BN + sub * HALF;
-      const int row = m0 + quarter * 32 + lane;
-      const bool ok = mbar_wait(&tfull[acc], (local >> 1) & 1, abort_flag, err, ERRBIT_TIMEOUT_GEMM);
-      if (!__all_sync(0xffffffffu, ok)) break;  // tcgen05.ld below is warp-collective
+      const int row0 = m0 + quarter * 32, row = row0 + lane;
+      if (!warp_wait(&tfull[acc], (local >> 1) & 1, abort_flag, err)) break;  // tcgen05.ld is warp-collective
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * S::ACC1 + sub * HALF;
       auto release = [&]() {
@@ -430,37 +497,64 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
       const int first = (S::OVERLAP != 0 && acc == 0) ? NCH / 2 : 0;  // chunk order: rotated for acc 0
       if (S::OVERLAP != 0 && !holds) release();
       uint32_t word = 0;
-      if (m0 + quarter * 32 < mpad) {
+      if (row0 < mpad) {
 #pragma unroll 1
-        for (int i = 0; i < NCH; ++i) {
-          const int ch = (i + first) & (NCH - 1);
-          const int col = n0 + ch * 32;
-          float v[32];
-          tmem_ld32(tb + ch * 32, v);
+        for (int i = 0; i < NCH; i += PER) {
+          const int ch0 = S::OVERLAP != 0 ? (i + first) & (NCH - 1) : i;
+          float v[PER][32];
+#pragma unroll
+          for (int k = 0; k < PER; ++k) tmem_ld32(tb + (ch0 + k) * 32, v[k]);
           tc_wait_ld();
-          if (holds && i == NCH / 2 - 1) release();
-          if (col < p.N && row < p.M) {
-            finish32(p, col, v);
-            if constexpr (OUT == MXO_F32) store32<float>(p, row, col, v);
-            if constexpr (OUT == MXO_BF16) store32<bf16>(p, row, col, v);
-            if constexpr (OUT == MXO_FP8) word |= store_block<MX_FP8>(p, row, col, v) << (8 * ch);
-            if constexpr (OUT == MXO_FP4) word |= store_block<MX_FP4>(p, row, col, v) << (8 * ch);
+          if (holds && i == 0) release();
+          if (S::OVERLAP == 0 && i + PER == NCH) release();
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            const int ch = ch0 + k, col = n0 + ch * 32, c0 = ch % GROUP * 32;
+            if ((i + k) % GROUP == 0 && p.tma) {  // the box's last store has read it
+              if (lane == 0) bulk_wait_read<0>();
+              __syncwarp();
+            }
+            if (col < p.N) {
+              finish32(p, col, v[k]);
+              const uint32_t byte = stage32<OUT, RB>(box, lane, c0, v[k]);
+              if (OUT >= MXO_FP8 && row < p.M) word |= byte << (8 * ch);
+            }
+            const int bcol = col - c0;
+            if ((i + k + 1) % GROUP == 0 && bcol < p.N && row0 < p.M) {
+              if (OUT >= MXO_FP8 || p.tma) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  tma_store_2d(&tmO, box, bcol / COLS * (RB / 4), row0);
+                  bulk_commit();
+                }
+              } else if constexpr (OUT < MXO_FP8) {
+                __syncwarp();
+                copy_box<OUT, RB, COLS>(p, box, row0, bcol, lane);
+                __syncwarp();
+              }
+            }
           }
         }
         if constexpr (OUT == MXO_FP8 || OUT == MXO_FP4) {
-          if ((n0 >> 7) < okt) {  // scales of this warp's columns; 0 beyond the tensor
+          if constexpr (NCH == 3) {
+            for (int ch = 0; ch < NCH; ++ch) {
+              const int blk = (n0 >> 5) + ch;
+              if ((blk >> 2) < okt) p.oscales[mx_scale_word(row, blk >> 2, okt) + (blk & 3)] = (uint8_t)(word >> (8 * ch));
+            }
+          } else if ((n0 >> 7) < okt) {  // scales of this warp's columns; 0 beyond the tensor
             uint8_t* dst = p.oscales + mx_scale_word(row, n0 >> 7, okt) + ((n0 >> 5) & 3);
             if constexpr (NCH == 4) *reinterpret_cast<uint32_t*>(dst) = word;
             if constexpr (NCH == 2) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)word;
             if constexpr (NCH == 1) *dst = (uint8_t)word;
           }
         }
-      } else if (holds) {
+      } else if (S::OVERLAP == 0 || holds) {
         release();
       }
-      if (S::OVERLAP == 0) release();
       if (*abort_flag) break;
     }
+    if (lane == 0) bulk_wait_all();  // the boxes outlive the stores, and the results are in memory
   }
 
   // every role ends here with its warp converged again, so the barrier counts each warp once
@@ -511,7 +605,7 @@ cudaError_t launch_mx(const MxMaps& maps, MxParams p, int K, int sms, cudaStream
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = PAIR ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemm_mx_kernel<F, BN, PAIR, OUT>, maps.a, maps.w, maps.sa, maps.sw, p,
+  return cudaLaunchKernelEx(&cfg, gemm_mx_kernel<F, BN, PAIR, OUT>, maps.a, maps.w, maps.sa, maps.sw, maps.o, p,
                             (unsigned*)nullptr);
 }
 
@@ -542,11 +636,17 @@ cudaError_t prepare_out() {
 
 }  // namespace
 
+// Every tile shape, for X(BN, PAIR)
+#define FH_MX_TILES(X) X(64, false) X(128, false) X(64, true) X(128, true) X(192, true) X(256, true)
+
 cudaError_t gemm_mx_prepare() {
-  const cudaError_t es[] = {prepare_out<MX_FP8, 128, false>(), prepare_out<MX_FP4, 128, false>()};
-  for (cudaError_t e : es)
-    if (e != cudaSuccess) return e;
-  return cudaSuccess;
+  cudaError_t e = cudaSuccess;
+#define FH_X(BNV, PAIRV)                                              \
+  if (e == cudaSuccess) e = prepare_out<MX_FP8, BNV, PAIRV>();        \
+  if (e == cudaSuccess) e = prepare_out<MX_FP4, BNV, PAIRV>();
+  FH_MX_TILES(FH_X)
+#undef FH_X
+  return e;
 }
 
 MxTile gemm_mx_tile(int M, int N, int K, int sms) {
@@ -557,6 +657,8 @@ MxTile gemm_mx_tile(int M, int N, int K, int sms) {
   return MxTile{128, false};
 }
 
+int gemm_mx_out_row_bytes(MxTile t, int out_kind) { return box_row_bytes(out_kind, t.bn / 2); }
+
 cudaError_t gemm_mx(const MxMaps& maps, MxTile t, const float* bias, void* out, void* oscales, int M, int N, int K,
                     int fmt, bool gelu, int out_kind, int sms, cudaStream_t st) {
   MxParams p = {};
@@ -566,9 +668,14 @@ cudaError_t gemm_mx(const MxMaps& maps, MxTile t, const float* bias, void* out, 
   p.M = M;
   p.N = N;
   p.gelu = gelu;
-  p.vec = ((long)N * (out_kind == MXO_F32 ? 4 : 2)) % 16 == 0;
-  return fmt == MX_FP8 ? launch_out<MX_FP8, 128, false>(maps, p, K, out_kind, sms, st)
-                       : launch_out<MX_FP4, 128, false>(maps, p, K, out_kind, sms, st);
+  p.tma = gemm_mx_tma_out(N, out_kind);
+#define FH_X(BNV, PAIRV)                                                                              \
+  if (t.bn == BNV && t.pair == PAIRV)                                                                 \
+    return fmt == MX_FP8 ? launch_out<MX_FP8, BNV, PAIRV>(maps, p, K, out_kind, sms, st)              \
+                         : launch_out<MX_FP4, BNV, PAIRV>(maps, p, K, out_kind, sms, st);
+  FH_MX_TILES(FH_X)
+#undef FH_X
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace fh
