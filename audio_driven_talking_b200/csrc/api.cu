@@ -1453,7 +1453,7 @@ int fh_op_linear_mx(const void* A, const void* A_scales, const void* W, const vo
   CK(cudaGetDevice(&dev));
   RUN(prepare_device(dev));
   CK(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  const MxTile t = gemm_mx_tile(M, N, K, sms);
+  const MxTile t = gemm_mx_tile(M, N, K, mx_fmt(mxtype), sms);
   const uint64_t pitch = mxtype == FH_MXFP4 ? K / 2 : K;
   const uint32_t kt = mxtype == FH_MXFP4 ? 2 : 1;
   MxMaps maps;

@@ -8,12 +8,16 @@
 // loop on 128-byte rows of codes, 128 values of mxfp8 or 256 of mxfp4, four MMAs of 32 bytes:
 //   warp 0     TMA producer: per stage the codes of A and W (128-byte swizzle) and their scale
 //              tiles (zero past the tensor, so a scale that the codes' padding meets is finite).
-//   warp 1     allocates TMEM; one thread copies a stage's scales to TMEM and issues the MMAs.
-//              The scale columns are double-buffered: a copy waits for the MMAs that read its
-//              buffer, so the tensor core always has a stage's MMAs queued.
+//   warp 1     allocates TMEM, copies each stage's scales there and issues the MMAs.
 //   warps 2-9  epilogue, two warps per TMEM lane quarter, each half of the tile's columns: bias,
 //              GELU, and fp32 or bf16 rows, or the microscaled form again: a thread holds 32
-//              consecutive values of a row, which is a block.
+//              consecutive values of a row, which is a block. Results leave by TMA from boxes
+//              in shared memory.
+// Warps 0 and 1 run their loops whole and elect a lane to issue: with one lane in a divergent
+// branch instead, issuing a stage's four MMAs took longer than running them (4096^3 mxfp8: 78.8 us
+// against 59.3). What bounds the loop now is shared memory: a stage's 32 KB are written by TMA and
+// read by the MMAs at 128 bytes a clock each SM, 512 of the about 600 clocks that a stage of a
+// 256 x 256 tile takes.
 // Every wait is bounded (FH_WAIT_LIMIT_NS), as in gemm_tc.cu.
 #include <type_traits>
 
@@ -26,14 +30,15 @@ namespace {
 
 constexpr int MXG_THREADS = 320;
 constexpr int EPI_THREADS = 256;
-constexpr uint32_t BOX_BYTES = 4096;  // of an epilogue warp: 32 rows of up to 128 bytes
+constexpr uint32_t BOX_BYTES = 4096;   // an epilogue warp's staging: one box of 32 rows x 128 bytes, or two of 64
+constexpr uint32_t BIAS_BYTES = 512;   // and its columns' bias
 
 enum MxOut { MXO_F32 = 0, MXO_BF16 = 1, MXO_FP8 = 2, MXO_FP4 = 3 };
 
-// Columns of a warp's staging box: 128 bytes of a row, as far as its share of the tile, `half`
-// columns, divides into boxes; a microscaled output's box is the whole share, in 32s if that is 96.
+// Columns of a staging box: 32, or what fills 64 bytes of a row where the warp's share of the
+// tile, `half` columns, divides into that.
 constexpr int box_cols(int out, int half) {
-  return out == MXO_F32 ? 32 : out == MXO_BF16 ? (half % 64 == 0 ? 64 : 32) : half % 64 == 0 ? half : 32;
+  return out == MXO_FP8 ? (half % 64 == 0 ? 64 : 32) : out == MXO_FP4 ? (half % 128 == 0 ? 128 : half % 64 == 0 ? 64 : 32) : 32;
 }
 constexpr int box_row_bytes(int out, int half) {
   return box_cols(out, half) * (out == MXO_F32 ? 8 : out == MXO_BF16 ? 4 : out == MXO_FP8 ? 2 : 1) / 2;
@@ -54,14 +59,6 @@ struct MxShape {
   static constexpr uint32_t SF_BYTES = SFA_BYTES + SFB_BYTES;
   static constexpr uint32_t STAGE_BYTES = OPER_BYTES + SF_BYTES;
   static constexpr uint32_t TX_BYTES = STAGE_BYTES * (PAIR ? 2 : 1);
-  static constexpr uint32_t OUT_BYTES = 8 * BOX_BYTES;  // the epilogue warps' staging boxes
-  static constexpr uint32_t AUX_BYTES = 1024;
-  static constexpr int FIT = (int)((227u * 1024u - 1024u - AUX_BYTES - OUT_BYTES) / STAGE_BYTES);
-  static constexpr int STAGES = FIT < 8 ? FIT : 8;
-  static constexpr uint32_t OUT_OFF = STAGES * OPER_BYTES;
-  static constexpr uint32_t SF_OFF = OUT_OFF + OUT_BYTES;
-  static constexpr uint32_t AUX_OFF = SF_OFF + STAGES * SF_BYTES;
-  static constexpr uint32_t SMEM = AUX_OFF + AUX_BYTES + 1024;
   // TMEM columns: two accumulators (at BN = 256 the second starts inside the first: see the
   // epilogue), then the scale buffers
   static constexpr int ACC1 = BN == 256 ? 192 : BN;
@@ -70,10 +67,21 @@ struct MxShape {
   static constexpr int SFA_COLS = 4 * ATOMS;
   static constexpr int SF_COLS = SFA_COLS + 4 * ATOMS * SFBT;
   static constexpr int NSF_FIT = (512 - SF_COL) / SF_COLS;
-  static constexpr int NSF = NSF_FIT < 4 ? NSF_FIT : 4;  // scale buffers
+  static constexpr uint32_t OUT_BYTES = 8 * (BOX_BYTES + BIAS_BYTES);  // the epilogue warps' staging
+  static constexpr uint32_t AUX_BYTES = 1024;
+  static constexpr int FIT = (int)((227u * 1024u - 1024u - AUX_BYTES - OUT_BYTES) / STAGE_BYTES);
+  static constexpr int STAGES = FIT < 8 ? FIT : 8;
+  // A scale buffer is free once the MMAs that read it are done. With one buffer per stage the
+  // stage's own barriers say so; where TMEM has room for fewer, the copy waits for the MMAs of
+  // the stage NSF before it.
+  static constexpr int NSF = NSF_FIT < STAGES ? NSF_FIT : STAGES;
+  static constexpr uint32_t OUT_OFF = STAGES * OPER_BYTES;
+  static constexpr uint32_t SF_OFF = OUT_OFF + OUT_BYTES;
+  static constexpr uint32_t AUX_OFF = SF_OFF + STAGES * SF_BYTES;
+  static constexpr uint32_t SMEM = AUX_OFF + AUX_BYTES + 1024;
   static constexpr uint32_t TMEM_COLS = 512;
   static_assert(NSF >= 2 && SF_COL + NSF * SF_COLS <= 512, "TMEM");
-  static_assert(STAGES > NSF, "a scale buffer's stage is still in the ring when it is reused");
+  static_assert(NSF <= STAGES, "a scale buffer's stage is still in the ring when it is reused");
 };
 
 // Matrix descriptor of a 512-byte scale tile for tcgen05.cp: 16-byte rows, no swizzle, groups
@@ -153,12 +161,61 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
     tc_commit(bar);
 }
 
-// The tanh form of GELU, x / (1 + e^(-2u)) with u = sqrt(2/pi) (x + 0.044715 x^3): the same
-// function as x (1 + tanh u) / 2. __expf is within a few 2^-22 relative here, far below the
-// rounding of every output type.
-__device__ __forceinline__ float gelu_sigmoid(float x) {
-  const float u2 = 1.5957691216057308f * fmaf(0.044715f * x, x * x, x);
-  return __fdividef(x, 1.f + __expf(-u2));
+// Two fp32 operations in one instruction
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+// The tanh form of GELU of four values, as x / (1 + 2^z) with z = -2 log2(e) sqrt(2/pi)
+// (x + 0.044715 x^3), which is x (1 + tanh u) / 2. The special-function unit (a quarter of a
+// warp instruction a clock) would bound it at 2^z and a reciprocal per value; one reciprocal of
+// the four denominators' product serves all of them: 10 clocks per value and scheduler instead
+// of 16. For the product to stay finite x is raised to -5.6 first, where the result is -3e-9:
+// below that the result is off by at most that much, 2^-28, and above it by a few 2^-22 relative.
+__device__ __forceinline__ void gelu4(float* v) {
+  float2 x[2], d[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    asm("max.NaN.f32 %0, %1, 0fC0B33333;" : "=f"(x[i].x) : "f"(v[2 * i]));
+    asm("max.NaN.f32 %0, %1, 0fC0B33333;" : "=f"(x[i].y) : "f"(v[2 * i + 1]));
+    const float2 k1 = make_float2(-2.3022082f, -2.3022082f), k3 = make_float2(-0.10294324f, -0.10294324f);
+    const float2 z = mul2(fma2(mul2(x[i], x[i]), k3, k1), x[i]);
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(z.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(z.y));
+    d[i] = add2(e, make_float2(1.f, 1.f));
+  }
+  const float ab = d[0].x * d[0].y, cd = d[1].x * d[1].y;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ab * cd));
+  const float2 q = mul2(make_float2(r, r), make_float2(cd, ab));  // 1 / ab, 1 / cd
+  const float2 y0 = mul2(x[0], mul2(make_float2(q.x, q.x), make_float2(d[0].y, d[0].x)));
+  const float2 y1 = mul2(x[1], mul2(make_float2(q.y, q.y), make_float2(d[1].y, d[1].x)));
+  v[0] = y0.x;
+  v[1] = y0.y;
+  v[2] = y1.x;
+  v[3] = y1.y;
 }
 
 struct MxParams {
@@ -172,28 +229,34 @@ struct MxParams {
   int tma;  // rows of out are 16-byte aligned: boxes leave by TMA
 };
 
-// One row's 32 consecutive results: bias, activation.
-__device__ __forceinline__ void finish32(const MxParams& p, int col, float (&v)[32]) {
-  if (p.bias) {
-    if (col + 32 <= p.N) {
+// One row's 32 consecutive results: bias (of these columns, in shared memory), activation.
+__device__ __forceinline__ void finish32(const MxParams& p, const float4* bias, float (&v)[32]) {
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 b = *reinterpret_cast<const float4*>(p.bias + col + j);
-        v[j] += b.x;
-        v[j + 1] += b.y;
-        v[j + 2] += b.z;
-        v[j + 3] += b.w;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (col + j < p.N) v[j] += p.bias[col + j];
-    }
+  for (int j = 0; j < 32; j += 4) {
+    const float4 b = bias[j / 4];
+    const float2 lo = add2(make_float2(v[j], v[j + 1]), make_float2(b.x, b.y));
+    const float2 hi = add2(make_float2(v[j + 2], v[j + 3]), make_float2(b.z, b.w));
+    v[j] = lo.x;
+    v[j + 1] = lo.y;
+    v[j + 2] = hi.x;
+    v[j + 3] = hi.y;
   }
   if (p.gelu) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = gelu_sigmoid(v[j]);
+    for (int j = 0; j < 32; j += 4) gelu4(v + j);
   }
+}
+
+// Columns col .. col + 4 of the bias; 0 past its end and where there is none
+__device__ __forceinline__ float4 load_bias(const MxParams& p, int col) {
+  float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.bias && col < p.N) {
+    if (col + 4 <= p.N) return *reinterpret_cast<const float4*>(p.bias + col);
+    b.x = p.bias[col];
+    if (col + 1 < p.N) b.y = p.bias[col + 1];
+    if (col + 2 < p.N) b.z = p.bias[col + 2];
+  }
+  return b;
 }
 
 // 16 bytes, unit `j` of a row of RB bytes, into a staging box as the TMA swizzle of that width has it
@@ -219,10 +282,7 @@ __device__ __forceinline__ uint32_t stage32(uint8_t* box, int row, int c0, const
     return 0;
   } else {
     constexpr MxFormat F = OUT == MXO_FP8 ? MX_FP8 : MX_FP4;
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 32; j += 8) m = max(m, mx_amax8(v + j));
-    const uint32_t byte = mx_scale_byte<F>(m);
+    const uint32_t byte = mx_scale_byte<F>(mx_amax32(v));
     uint2 c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) c[j] = mx_encode8<F>(v + 8 * j, byte);
@@ -261,6 +321,19 @@ __device__ __forceinline__ bool elect_one() {
 // mbar_wait (common.cuh: bounded, false on giving up) by a whole warp, with one answer
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err) {
   return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || mbar_wait(bar, parity, abort, err, ERRBIT_TIMEOUT_GEMM));
+}
+
+// Whether the phase is complete, without waiting
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // A place in a ring of N barriers
@@ -406,8 +479,9 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
   } else if (warp == 1) {
     if (rank == 0) {
       Ring<S::STAGES> cur, done;  // the stage to issue, and the one whose MMAs free its scale buffer
-      int sfi = 0, local = 0;
+      int sf_next = 0, local = 0;
       int pending = 0;  // stages issued, up to NSF
+      bool ready = false;
       const uint64_t ad0 = sdesc_kmajor_sw128(smem_u32(smem));
       const uint64_t bd0 = sdesc_kmajor_sw128(smem_u32(smem) + S::A_BYTES);
       const uint64_t sd0 = sdesc_scales(smem_u32(smem) + S::SF_OFF);
@@ -426,20 +500,24 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
         // the tile's first W row within its scale row tile (BN = 64, 192): 32 rows a column
         const uint32_t sfb_off = BN % 128 != 0 ? (uint32_t)((((tile / p.num_m) * BN) & 127) >> 5) : 0u;
         for (int kb = 0; kb < p.nk; ++kb) {
-          // the scale buffer is free once the MMAs of the stage NSF before this one are done
-          if (pending == S::NSF) {
-            ok = warp_wait(&empty[done.i], done.phase, abort_flag, err);
-            done.next();
-          } else {
-            ++pending;
+          if constexpr (S::NSF < S::STAGES) {
+            if (pending == S::NSF) {
+              ok = warp_wait(&empty[done.i], done.phase, abort_flag, err);
+              done.next();
+            } else {
+              ++pending;
+            }
           }
-          ok = ok && warp_wait(&full[cur.i], cur.phase, abort_flag, err);
+          ok = ok && (__all_sync(0xffffffffu, ready) || warp_wait(&full[cur.i], cur.phase, abort_flag, err));
           if (!ok) break;
+          const int sfi = S::NSF < S::STAGES ? sf_next : cur.i, stage = cur.i;
+          cur.next();
+          ready = mbar_test(&full[cur.i], cur.phase);  // the next stage's, under this one's issue
           tc_fence_after();
           if (elect_one()) {
             const uint32_t sf = tmem_base + S::SF_COL + sfi * S::SF_COLS;
-            const uint64_t ad = ad0 + cur.i * (S::OPER_BYTES >> 4), bd = bd0 + cur.i * (S::OPER_BYTES >> 4);
-            issue_scales<F, BN, PAIR>(sd0 + cur.i * (S::SF_BYTES >> 4), sf);
+            const uint64_t ad = ad0 + stage * (S::OPER_BYTES >> 4), bd = bd0 + stage * (S::OPER_BYTES >> 4);
+            issue_scales<F, BN, PAIR>(sd0 + stage * (S::SF_BYTES >> 4), sf);
             issue_mma<F, BN, PAIR>(0, d_tmem, ad, bd, sf, sfb_off, kb > 0);
             if (kb + 1 < p.nk || p.last == 4) {
 #pragma unroll
@@ -448,12 +526,11 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
               if (p.last > 1) issue_mma<F, BN, PAIR>(1, d_tmem, ad, bd, sf, sfb_off, 1u);
               if (p.last > 2) issue_mma<F, BN, PAIR>(2, d_tmem, ad, bd, sf, sfb_off, 1u);
             }
-            commit<PAIR>(&empty[cur.i]);
+            commit<PAIR>(&empty[stage]);
             if (kb + 1 == p.nk) commit<PAIR>(&tfull[acc]);
           }
           __syncwarp();
-          cur.next();
-          if (++sfi == S::NSF) sfi = 0;
+          if (++sf_next == S::NSF) sf_next = 0;
         }
         if (!ok) break;
       }
@@ -472,13 +549,17 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
     constexpr int COLS = box_cols(OUT, HALF), RB = box_row_bytes(OUT, HALF), GROUP = COLS / 32;
     const long okt = (p.N + 127) >> 7;
     const int mpad = (p.M + 127) & ~127;
-    uint8_t* box = smem + S::OUT_OFF + (warp - 2) * BOX_BYTES;
+    constexpr int BOXES = 32 * RB * 2 <= (int)BOX_BYTES ? 2 : 1;  // used in turn
+    uint8_t* const boxes = smem + S::OUT_OFF + (warp - 2) * BOX_BYTES;
+    float4* const bias = reinterpret_cast<float4*>(smem + S::OUT_OFF + 8 * BOX_BYTES + (warp - 2) * BIAS_BYTES);
     pdl_wait();
-    int local = 0;
+    int local = 0, turn = 0;
     for (int tile = cl; tile < p.ntiles; tile += ncl, ++local) {
       const int acc = local & 1;
       const int m0 = (tile % p.num_m) * S::TM + (int)rank * 128;
       const int n0 = (tile / p.num_m) * BN + sub * HALF;
+      if (lane < HALF / 4) bias[lane] = load_bias(p, n0 + 4 * lane);  // while the MMAs run
+      __syncwarp();
       const int row0 = m0 + quarter * 32, row = row0 + lane;
       if (!warp_wait(&tfull[acc], (local >> 1) & 1, abort_flag, err)) break;  // tcgen05.ld is warp-collective
       tc_fence_after();
@@ -510,12 +591,13 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
 #pragma unroll
           for (int k = 0; k < PER; ++k) {
             const int ch = ch0 + k, col = n0 + ch * 32, c0 = ch % GROUP * 32;
+            uint8_t* box = boxes + turn * (BOX_BYTES / 2);
             if ((i + k) % GROUP == 0 && p.tma) {  // the box's last store has read it
-              if (lane == 0) bulk_wait_read<0>();
+              if (lane == 0) bulk_wait_read<BOXES - 1>();
               __syncwarp();
             }
             if (col < p.N) {
-              finish32(p, col, v[k]);
+              finish32(p, bias + ch * 8, v[k]);
               const uint32_t byte = stage32<OUT, RB>(box, lane, c0, v[k]);
               if (OUT >= MXO_FP8 && row < p.M) word |= byte << (8 * ch);
             }
@@ -528,6 +610,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
                   tma_store_2d(&tmO, box, bcol / COLS * (RB / 4), row0);
                   bulk_commit();
                 }
+                if (BOXES == 2) turn ^= 1;
               } else if constexpr (OUT < MXO_FP8) {
                 __syncwarp();
                 copy_box<OUT, RB, COLS>(p, box, row0, bcol, lane);
@@ -552,6 +635,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
       } else if (S::OVERLAP == 0 || holds) {
         release();
       }
+      __syncwarp();  // the bias is read
       if (*abort_flag) break;
     }
     if (lane == 0) bulk_wait_all();  // the boxes outlive the stores, and the results are in memory
@@ -637,7 +721,7 @@ cudaError_t prepare_out() {
 }  // namespace
 
 // Every tile shape, for X(BN, PAIR)
-#define FH_MX_TILES(X) X(64, false) X(128, false) X(64, true) X(128, true) X(192, true) X(256, true)
+#define FH_MX_TILES(X) X(64, false) X(128, false) X(128, true) X(192, true) X(256, true)
 
 cudaError_t gemm_mx_prepare() {
   cudaError_t e = cudaSuccess;
@@ -649,12 +733,35 @@ cudaError_t gemm_mx_prepare() {
   return e;
 }
 
-MxTile gemm_mx_tile(int M, int N, int K, int sms) {
-  (void)M;
-  (void)N;
-  (void)K;
-  (void)sms;
-  return MxTile{128, false};
+// The tile shape with the least estimated time. Tiles are dealt out in rounds, one per CTA or CTA
+// pair; a round takes a fixed part and a part per stage, measured in back-to-back launches of
+// 4096 x 4096 x {4096 mxfp8, 8192 mxfp4}, 8640 x 4608 x 1536 mxfp8 and 23040 x 8960 x 1536 mxfp4
+// (us): wide tiles read fewer operand bytes per MMA and win where there are many rounds (the
+// last shape: 146 us at 256 columns on pairs, 159 at 128), narrow ones where a round of wide ones
+// would leave SMs idle (1280 x 1536 x 8960 mxfp4: 11.0 us at 128 columns, 14.4 at 256).
+MxTile gemm_mx_tile(int M, int N, int K, int fmt, int sms) {
+  static const struct {
+    MxTile t;
+    float stage[2], fixed;
+  } shapes[] = {{{64, false}, {0.238f, 0.252f}, 0.33f},
+                {{128, false}, {0.270f, 0.283f}, 0.45f},
+                {{128, true}, {0.234f, 0.228f}, 0.52f},
+                {{192, true}, {0.281f, 0.324f}, 0.75f},
+                {{256, true}, {0.336f, 0.326f}, 1.45f}};
+  const int kb = fmt == MX_FP8 ? 128 : 256, nk = (K + kb - 1) / kb;
+  MxTile best = shapes[0].t;
+  float least = 0.f;
+  for (const auto& s : shapes) {
+    const int tm = s.t.pair ? 256 : 128, slots = s.t.pair ? sms / 2 : sms;
+    if (slots < 1) continue;
+    const long tiles = (long)((M + tm - 1) / tm) * ((N + s.t.bn - 1) / s.t.bn);
+    const float us = (float)((tiles + slots - 1) / slots) * (nk * s.stage[fmt] + s.fixed);
+    if (least == 0.f || us < least) {
+      least = us;
+      best = s.t;
+    }
+  }
+  return best;
 }
 
 int gemm_mx_out_row_bytes(MxTile t, int out_kind) { return box_row_bytes(out_kind, t.bn / 2); }

@@ -65,12 +65,23 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float* v) {
   return r;
 }
 
-// largest |v| of eight, as a bit pattern
+// Largest |v|, as a bit pattern: NaN (0x7fffffff) if any is, by three-way maxima
+__device__ __forceinline__ float amax3(float m, float a, float b) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ uint32_t mx_amax8(const float* v) {
-  uint32_t m = 0;
+  float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-  return m;
+  for (int i = 0; i < 8; i += 2) m = amax3(m, v[i], v[i + 1]);
+  return __float_as_uint(m);
+}
+__device__ __forceinline__ uint32_t mx_amax32(const float* v) {
+  float m[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m[j] = __uint_as_float(mx_amax8(v + 8 * j));
+  return __float_as_uint(amax3(amax3(m[0], m[1], m[2]), m[3], 0.f));
 }
 
 // Codes of eight values under a scale byte: 8 bytes (e4m3) or 4 bytes (e2m1, in .x).
