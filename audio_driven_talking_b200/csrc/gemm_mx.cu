@@ -30,16 +30,14 @@ namespace {
 
 constexpr int MXG_THREADS = 320;
 constexpr int EPI_THREADS = 256;
-constexpr uint32_t BOX_BYTES = 4096;   // an epilogue warp's staging: one box of 32 rows x 128 bytes, or two of 64
+constexpr uint32_t BOX_BYTES = 4096;   // an epilogue warp's staging box: 32 rows of up to 128 bytes
 constexpr uint32_t BIAS_BYTES = 512;   // and its columns' bias
 
 enum MxOut { MXO_F32 = 0, MXO_BF16 = 1, MXO_FP8 = 2, MXO_FP4 = 3 };
 
-// Columns of a staging box: 32, or what fills 64 bytes of a row where the warp's share of the
-// tile, `half` columns, divides into that.
-constexpr int box_cols(int out, int half) {
-  return out == MXO_FP8 ? (half % 64 == 0 ? 64 : 32) : out == MXO_FP4 ? (half % 128 == 0 ? 128 : half % 64 == 0 ? 64 : 32) : 32;
-}
+// Columns that an epilogue warp takes at a time, of its share `half` of the tile: 64 where that
+// divides and a row of them fits the box.
+constexpr int box_cols(int out, int half) { return out != MXO_F32 && half % 64 == 0 ? 64 : 32; }
 constexpr int box_row_bytes(int out, int half) {
   return box_cols(out, half) * (out == MXO_F32 ? 8 : out == MXO_BF16 ? 4 : out == MXO_FP8 ? 2 : 1) / 2;
 }
@@ -545,15 +543,14 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
     const int sub = (warp - 2) >> 2;  // which half of the tile's columns
     constexpr int HALF = BN / 2;
     constexpr int NCH = HALF / 32;              // chunks of 32 columns
-    constexpr int PER = NCH % 2 == 0 ? 2 : 1;   // chunks read from TMEM at once
-    constexpr int COLS = box_cols(OUT, HALF), RB = box_row_bytes(OUT, HALF), GROUP = COLS / 32;
+    constexpr int COLS = box_cols(OUT, HALF), RB = box_row_bytes(OUT, HALF);
+    constexpr int PER = COLS / 32;              // chunks taken at a time
     const long okt = (p.N + 127) >> 7;
     const int mpad = (p.M + 127) & ~127;
-    constexpr int BOXES = 32 * RB * 2 <= (int)BOX_BYTES ? 2 : 1;  // used in turn
-    uint8_t* const boxes = smem + S::OUT_OFF + (warp - 2) * BOX_BYTES;
+    uint8_t* const box = smem + S::OUT_OFF + (warp - 2) * BOX_BYTES;
     float4* const bias = reinterpret_cast<float4*>(smem + S::OUT_OFF + 8 * BOX_BYTES + (warp - 2) * BIAS_BYTES);
     pdl_wait();
-    int local = 0, turn = 0;
+    int local = 0;
     for (int tile = cl; tile < p.ntiles; tile += ncl, ++local) {
       const int acc = local & 1;
       const int m0 = (tile % p.num_m) * S::TM + (int)rank * 128;
@@ -582,41 +579,36 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
 #pragma unroll 1
         for (int i = 0; i < NCH; i += PER) {
           const int ch0 = S::OVERLAP != 0 ? (i + first) & (NCH - 1) : i;
+          const int col = n0 + ch0 * 32;
           float v[PER][32];
 #pragma unroll
           for (int k = 0; k < PER; ++k) tmem_ld32(tb + (ch0 + k) * 32, v[k]);
           tc_wait_ld();
-          if (holds && i == 0) release();
+          if (holds && i + PER == NCH / 2) release();
           if (S::OVERLAP == 0 && i + PER == NCH) release();
+          if (col >= p.N || row0 >= p.M) continue;  // nothing of the tensor
+#pragma unroll
+          for (int k = 0; k < PER; ++k) finish32(p, bias + (ch0 + k) * 8, v[k]);
+          if (p.tma) {  // the box's last store has read it
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+          }
 #pragma unroll
           for (int k = 0; k < PER; ++k) {
-            const int ch = ch0 + k, col = n0 + ch * 32, c0 = ch % GROUP * 32;
-            uint8_t* box = boxes + turn * (BOX_BYTES / 2);
-            if ((i + k) % GROUP == 0 && p.tma) {  // the box's last store has read it
-              if (lane == 0) bulk_wait_read<BOXES - 1>();
-              __syncwarp();
+            const uint32_t byte = stage32<OUT, RB>(box, lane, 32 * k, v[k]);
+            if (OUT >= MXO_FP8 && row < p.M && col + 32 * k < p.N) word |= byte << (8 * (ch0 + k));
+          }
+          if (OUT >= MXO_FP8 || p.tma) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tmO, box, col / COLS * (RB / 4), row0);
+              bulk_commit();
             }
-            if (col < p.N) {
-              finish32(p, bias + ch * 8, v[k]);
-              const uint32_t byte = stage32<OUT, RB>(box, lane, c0, v[k]);
-              if (OUT >= MXO_FP8 && row < p.M) word |= byte << (8 * ch);
-            }
-            const int bcol = col - c0;
-            if ((i + k + 1) % GROUP == 0 && bcol < p.N && row0 < p.M) {
-              if (OUT >= MXO_FP8 || p.tma) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                  tma_store_2d(&tmO, box, bcol / COLS * (RB / 4), row0);
-                  bulk_commit();
-                }
-                if (BOXES == 2) turn ^= 1;
-              } else if constexpr (OUT < MXO_FP8) {
-                __syncwarp();
-                copy_box<OUT, RB, COLS>(p, box, row0, bcol, lane);
-                __syncwarp();
-              }
-            }
+          } else if constexpr (OUT < MXO_FP8) {
+            __syncwarp();
+            copy_box<OUT, RB, COLS>(p, box, row0, col, lane);
+            __syncwarp();
           }
         }
         if constexpr (OUT == MXO_FP8 || OUT == MXO_FP4) {
