@@ -356,11 +356,10 @@ class MXTensor:
     def empty(cls, rows: int, cols: int, fmt: str, device) -> "MXTensor":
         """Room for rows x cols values, not initialised."""
         import torch
-        pitch = cols if _format(fmt) == FH_MXFP8 else cols // 2
-        n = -(-rows // 128) * -(-cols // 128) * 512
-        # empty_strided: the cheapest of torch's allocations (1.5 us where torch.empty takes 2.3)
-        return cls(torch.empty_strided((rows, pitch), (pitch, 1), dtype=torch.uint8, device=device),
-                   torch.empty_strided((n,), (1,), dtype=torch.uint8, device=device), (rows, cols), fmt)
+        if fmt not in FORMATS:
+            raise ValueError(f"format {fmt!r}: expected one of {sorted(FORMATS)}")
+        return cls(torch.empty((rows, cols if fmt == "mxfp8" else cols // 2), dtype=torch.uint8, device=device),
+                   torch.empty(cls.scale_bytes(rows, cols), dtype=torch.uint8, device=device), (rows, cols), fmt)
 
     @property
     def device(self):
@@ -370,111 +369,49 @@ class MXTensor:
         return f"MXTensor({self.shape[0]} x {self.shape[1]}, {self.fmt}, {self.device})"
 
 
-def _format(fmt) -> int:
-    code = FORMATS.get(fmt)
-    if code is None:
-        raise ValueError(f"format {fmt!r}: expected one of {sorted(FORMATS)}")
-    return code
+def _load_bind():
+    """The binding module of the operators below (``_fhbind.so``, built in-tree with libfh.so)."""
+    global _bind
+    import importlib.util
+
+    import torch  # noqa: F401  (the module links to its libraries)
+    load_library()
+    path = os.path.join(_HERE, "_fhbind.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with `python -m audio_driven_talking_b200.build`; "
+                          "there is no fallback implementation")
+    spec = importlib.util.spec_from_file_location("_fhbind", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.init(MXTensor, FHError)
+    _bind = mod
+    return mod
 
 
-def _kind(dtype, what: str) -> int:
+_bind = None
+
+
+def _on_stream(stream, first, inputs, call):
+    """``call()`` on `stream` (a torch stream or a handle) of the device of `first`: its outputs are
+    allocated there, and the inputs' memory is kept until its work is done."""
     import torch
-    if dtype is torch.float32:
-        return FH_F32
-    if dtype is torch.bfloat16:
-        return FH_BF16
-    raise TypeError(f"{what}: expected float32 or bfloat16, got {dtype}")
-
-
-def _out_kind(out) -> int:
-    import torch
-    if out is torch.bfloat16:
-        return FH_BF16
-    if out is torch.float32:
-        return FH_F32
-    code = FORMATS.get(out) if isinstance(out, str) else None
-    if code is None:
-        raise ValueError(f"out={out!r}: expected torch.float32, torch.bfloat16, 'mxfp8' or 'mxfp4'")
-    return code
-
-
-def _cuda_index(t, what: str) -> int:
-    """The device of a CUDA tensor."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what}: expected a torch tensor")
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{what}: expected a CUDA tensor")
-    return dev
-
-
-def _same_device(t, what: str, device: int):
-    dev = _cuda_index(t, what)
-    if dev != device:
-        raise ValueError(f"{what} is on cuda:{dev}, expected cuda:{device}")
-
-
-def _matrix(t, what: str):
-    if t.dim() != 2:
-        raise ValueError(f"{what}: expected 2 dimensions, got {t.dim()}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-
-
-def _vector(t, what: str, n: int, device: int):
-    import torch
-    _same_device(t, what, device)
-    if t.dtype is not torch.float32 or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{what}: expected contiguous float32 [{n}]")
-
-
-def _mx_operand(q, what: str, device: int = -1):
-    """(format code, device) of a microscaled operand, checked."""
-    import torch
-    if not isinstance(q, MXTensor):
-        raise TypeError(f"{what}: expected an MXTensor")
-    code = _format(q.fmt)
-    rows, cols = q.shape
-    if rows < 1 or cols < 32 or cols % 32:
-        raise ValueError(f"{what}: {rows} x {cols} is not a microscaled shape (columns: a multiple of 32)")
-    u8, d, s = torch.uint8, q.data, q.scales
-    dev = _cuda_index(d, f"{what}.data")
-    if device >= 0 and dev != device:
-        raise ValueError(f"{what}.data is on cuda:{dev}, expected cuda:{device}")
-    n, ns = rows * cols // (2 if code == FH_MXFP4 else 1), -(-rows // 128) * -(-cols // 128) * 512
-    if d.dtype is not u8 or d.numel() != n or not d.is_contiguous():
-        raise ValueError(f"{what}.data: expected {n} contiguous uint8 values")
-    if _cuda_index(s, f"{what}.scales") != dev or s.dtype is not u8 or s.numel() != ns or not s.is_contiguous():
-        raise ValueError(f"{what}.scales: expected {ns} contiguous uint8 values on cuda:{dev}")
-    return code, dev
-
-
-def _elsewhere(device: int, stream, inputs, call):
-    """``call()`` with `device` current and, where `stream` (a torch stream or a handle) is given, on that
-    stream: its outputs are allocated there, and the inputs' memory is kept until its work is done."""
-    import torch
-    if stream is None:
-        with torch.cuda.device(device):
-            return call()
+    if isinstance(first, MXTensor):
+        first = first.data
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        return call()  # refuses it
+    device = first.get_device()
     if not isinstance(stream, torch.cuda.Stream):
         stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
                   else torch.cuda.default_stream(device))
     if stream.device_index != device:
         raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the tensors to cuda:{device}")
-    with torch.cuda.stream(stream):  # makes the stream's device current too
+    with torch.cuda.stream(stream):
         out = call()
         for t in inputs:
-            if t is not None:
-                t.record_stream(stream)
+            for part in ((t.data, t.scales) if isinstance(t, MXTensor) else (t,)):
+                if part is not None:
+                    part.record_stream(stream)
     return out
-
-
-def _current(device: int):
-    """The handle of torch's current stream on `device`, or None where another device is current.
-    (current_stream() builds a Python object: 3.2 us a call, where the handle alone takes 0.1.)"""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device) if torch.cuda.current_device() == device else None
 
 
 def quantize(x, fmt="mxfp8", stream=None):
@@ -484,38 +421,21 @@ def quantize(x, fmt="mxfp8", stream=None):
     Each block's scale is the smallest power of two (2^-127 or more) under which nothing in it
     saturates; elements round to nearest, ties to even. A block with an infinity or a NaN reads
     back as NaN."""
-    code = _format(fmt)
-    dev = _cuda_index(x, "x")
-    kind = _kind(x.dtype, "x")
-    if x.dim() != 2 or x.stride(1) != 1:
-        raise ValueError("x: expected 2 dimensions with contiguous rows")
-    M, K = x.shape
-    handle = _current(dev) if stream is None else None
-    if handle is None:
-        return _elsewhere(dev, stream, (x,), lambda: quantize(x, fmt))
-    q = MXTensor.empty(M, K, fmt, x.device)
-    rc = load_library().fh_op_quantize(x.data_ptr(), x.stride(0) if M > 1 else K, M, K, kind, code, q.data.data_ptr(),
-                                       q.scales.data_ptr(), handle)
-    if rc:
-        _check(rc)
-    return q
+    bind = _bind or _load_bind()
+    if stream is None:
+        return bind.quantize(x, fmt)
+    return _on_stream(stream, x, (x,), lambda: bind.quantize(x, fmt))
 
 
 def dequantize(q, dtype=None, stream=None):
     """The values of a microscaled tensor, float32 (the default) or bfloat16 [rows, columns]."""
-    import torch
-    code, dev = _mx_operand(q, "q")
-    dtype = dtype or torch.float32
-    kind = _kind(dtype, "dtype")
-    M, K = q.shape
-    handle = _current(dev) if stream is None else None
-    if handle is None:
-        return _elsewhere(dev, stream, (q.data, q.scales), lambda: dequantize(q, dtype))
-    out = torch.empty_strided((M, K), (K, 1), dtype=dtype, device=q.data.device)
-    rc = load_library().fh_op_dequantize(q.data.data_ptr(), q.scales.data_ptr(), M, K, code, out.data_ptr(), kind, handle)
-    if rc:
-        _check(rc)
-    return out
+    bind = _bind or _load_bind()
+    if dtype is None:
+        import torch
+        dtype = torch.float32
+    if stream is None:
+        return bind.dequantize(q, dtype)
+    return _on_stream(stream, q, (q,), lambda: bind.dequantize(q, dtype))
 
 
 def add_rms_norm(x, res, a, c=None, out="mxfp8", eps=1e-6, sum_out=None, stream=None):
@@ -527,47 +447,10 @@ def add_rms_norm(x, res, a, c=None, out="mxfp8", eps=1e-6, sum_out=None, stream=
     [streams, columns] where each of `streams` equal runs of rows has its own. Columns are a
     multiple of 32, at most 16384. The sum goes to a new tensor, or to `sum_out`, which may be x
     itself (or res, where the types agree)."""
-    import torch
-    kind = _out_kind(out)
-    dev = _cuda_index(x, "x")
-    _same_device(res, "res", dev)
-    _matrix(x, "x")
-    _matrix(res, "res")
-    M, D = x.shape
-    if res.shape != x.shape:
-        raise ValueError(f"res: expected shape {tuple(x.shape)}, got {tuple(res.shape)}")
-    _same_device(a, "a", dev)
-    streams = a.shape[0] if a.dim() == 2 else 1
-    if a.dtype is not torch.float32 or a.dim() not in (1, 2) or a.shape[-1] != D or not a.is_contiguous():
-        raise ValueError(f"a: expected contiguous float32 [{D}] or [streams, {D}]")
-    if streams < 1 or M % streams:
-        raise ValueError(f"{M} rows do not divide into {streams} streams")
-    if c is not None:
-        _same_device(c, "c", dev)
-        if c.dtype is not torch.float32 or c.shape != a.shape or not c.is_contiguous():
-            raise ValueError("c: expected a contiguous float32 tensor of a's shape")
-    if sum_out is not None:
-        _same_device(sum_out, "sum_out", dev)
-        _matrix(sum_out, "sum_out")
-        if sum_out.shape != x.shape or sum_out.dtype is not x.dtype:
-            raise ValueError("sum_out: expected x's shape and type")
-    xk, rk = _kind(x.dtype, "x"), _kind(res.dtype, "res")
-    handle = _current(dev) if stream is None else None
-    if handle is None:
-        return _elsewhere(dev, stream, (x, res, a, c, sum_out), lambda: add_rms_norm(x, res, a, c, out, eps, sum_out))
-    total = torch.empty_like(x) if sum_out is None else sum_out
-    if kind >= FH_MXFP8:
-        y = MXTensor.empty(M, D, out, x.device)
-        data, scales = y.data.data_ptr(), y.scales.data_ptr()
-    else:
-        y = torch.empty_strided((M, D), (D, 1), dtype=out, device=x.device)
-        data, scales = y.data_ptr(), None
-    rc = load_library().fh_op_add_rms_norm(x.data_ptr(), xk, res.data_ptr(), rk, total.data_ptr(), a.data_ptr(),
-                                           None if c is None else c.data_ptr(), D if streams > 1 else 0,
-                                           M // streams or 1, M, D, eps, kind, data, scales, handle)
-    if rc:
-        _check(rc)
-    return total, y
+    bind = _bind or _load_bind()
+    if stream is None:
+        return bind.add_rms_norm(x, res, a, c, out, eps, sum_out)
+    return _on_stream(stream, x, (x, res, a, c, sum_out), lambda: bind.add_rms_norm(x, res, a, c, out, eps, sum_out))
 
 
 def linear_mx(A, W, bias=None, act=None, out=None, stream=None):
@@ -577,37 +460,10 @@ def linear_mx(A, W, bias=None, act=None, out=None, stream=None):
     form). The result has the type that `out` names: torch.bfloat16 (the default),
     torch.float32, or "mxfp8" / "mxfp4" (columns a multiple of 32), an operand of the next
     product; sums are kept in float32."""
-    import torch
-    out = torch.bfloat16 if out is None else out
-    kind = _out_kind(out)
-    if act is not None and act != "gelu":
-        raise ValueError(f"act={act!r}: expected None or 'gelu'")
-    code, dev = _mx_operand(A, "A")
-    if _mx_operand(W, "W", dev)[0] != code:
-        raise ValueError(f"A is {A.fmt}, W is {W.fmt}: expected one format")
-    (M, K), (N, KW) = A.shape, W.shape
-    if K != KW:
-        raise ValueError(f"A has {K} columns, W has {KW}")
-    if bias is not None:
-        _vector(bias, "bias", N, dev)
-    if kind >= FH_MXFP8 and N % 32:
-        raise ValueError(f"{N} columns: a microscaled output needs a multiple of 32")
-    handle = _current(dev) if stream is None else None
-    if handle is None:
-        return _elsewhere(dev, stream, (A.data, A.scales, W.data, W.scales, bias),
-                          lambda: linear_mx(A, W, bias, act, out))
-    if kind >= FH_MXFP8:
-        y = MXTensor.empty(M, N, out, A.data.device)
-        data, scales = y.data.data_ptr(), y.scales.data_ptr()
-    else:
-        y = torch.empty_strided((M, N), (N, 1), dtype=out, device=A.data.device)
-        data, scales = y.data_ptr(), None
-    rc = load_library().fh_op_linear_mx(A.data.data_ptr(), A.scales.data_ptr(), W.data.data_ptr(), W.scales.data_ptr(),
-                                        None if bias is None else bias.data_ptr(), M, N, K, code,
-                                        FH_ACT_NONE if act is None else FH_ACT_GELU, kind, data, scales, handle)
-    if rc:
-        _check(rc)
-    return y
+    bind = _bind or _load_bind()
+    if stream is None:
+        return bind.linear_mx(A, W, bias, act, out)
+    return _on_stream(stream, A, (A, W, bias), lambda: bind.linear_mx(A, W, bias, act, out))
 
 
 __all__ = ["DiT", "ModelConfig", "LITE", "FP32_BLOCK", "ONE_BLOCK", "LITE_768_X3", "FHError", "load_library",
