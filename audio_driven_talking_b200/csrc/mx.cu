@@ -7,67 +7,114 @@ namespace fh {
 
 namespace {
 
-// ------------------------------------------------------------------ quantise / dequantise
-// One CTA per tile of 128 rows x 128 columns, i.e. per 512-byte scale tile. Sixteen lanes take a
-// row's 128 columns, 8 values each; four lanes make a block, whose maximum crosses them by two
-// shuffles. Bytes bound it: the values read once, the codes and scales written once.
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
+
+// Eight consecutive values: fp32 in one access, which fills whole sectors, where `wide` says that they
+// lie on 32 bytes
+__device__ __forceinline__ void store8w(bf16* p, const float (&v)[8], bool) { store8(p, v); }
+__device__ __forceinline__ void store8w(float* p, const float (&v)[8], bool wide) {
+  if (wide)
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+  else
+    store8(p, v);
+}
+
+// ------------------------------------------------------------------ quantise
+// A warp takes units of 4 rows x 128 columns, 16 columns a lane: two lanes make a block, so its
+// maximum crosses lanes once, and the four scale bytes of a row are one word. QU units are loaded
+// before the first is worked on, and no warp waits for another. Bytes bound it: the values read
+// once, the codes and scales written once.
 constexpr int QT_THREADS = 256;
 
-template <typename T, MxFormat F>
+// Sixteen consecutive values as they lie in memory: 4 * sizeof(T) words
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, uint32_t (&w)[4 * sizeof(T)]) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T); ++i) {
+    const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+    w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void unpack16(const uint32_t (&w)[4 * sizeof(T)], float (&v)[16]) {
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
+  }
+}
+template <typename T, MxFormat F, int QU>
 __global__ void __launch_bounds__(QT_THREADS) quantize_kernel(const T* __restrict__ x, long ldx, int M, int K,
+                                                              unsigned ktiles, unsigned units,
                                                               uint8_t* __restrict__ data,
                                                               uint8_t* __restrict__ scales) {
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int PER = F == MX_FP8 ? 8 : 4;  // code bytes of 8 values
-  const int ktiles = (K + 127) >> 7;
-  const int kt = blockIdx.x % ktiles, rt = blockIdx.x / ktiles;
-  const int lane16 = threadIdx.x & 15, hw = threadIdx.x >> 4;  // 16 half-warps
-  const int col = kt * 128 + lane16 * 8;
-  const long rowb = (long)K * PER / 8;
-  __shared__ __align__(16) uint32_t words[128];  // the scale tile
-  float v[8][8];
+  const int lane = threadIdx.x & 31, seg = lane & 7;
+  const unsigned u0 = (blockIdx.x * (QT_THREADS / 32) + (threadIdx.x >> 5)) * QU;
+  unsigned rg = u0 / ktiles, kt = u0 - rg * ktiles;
+  uint32_t raw[QU][4 * sizeof(T)];
+  int row[QU], tile[QU];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const long r = (long)rt * 128 + hw + 16 * i;
-    if (r < M && col < K) {
-      load8(x + r * ldx + col, v[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+  for (int i = 0; i < QU; ++i) {
+    row[i] = u0 + i < units ? (int)(rg * 4 + (lane >> 3)) : -1;
+    tile[i] = kt;
+    if (++kt == ktiles) {
+      kt = 0;
+      ++rg;
     }
+#pragma unroll
+    for (int j = 0; j < 4 * (int)sizeof(T); ++j) raw[i][j] = 0u;
+    const int col = tile[i] * 128 + seg * 16;
+    if (row[i] >= 0 && row[i] < M && col < K) load16<T>(x + (long)row[i] * ldx + col, raw[i]);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int rl = hw + 16 * i;
-    const long r = (long)rt * 128 + rl;
-    uint32_t m = mx_amax8(v[i]);
+  for (int i = 0; i < QU; ++i) {
+    float v[16];
+    unpack16<T>(raw[i], v);
+    uint32_t m = max(mx_amax8(v), mx_amax8(v + 8));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const uint32_t byte = mx_scale_byte<F>(m);  // 0 for the zeros beyond the tensor
-    uint32_t w = byte << (8 * (lane16 >> 2));
+    uint32_t w = byte << (8 * (seg >> 1));
+    w |= __shfl_xor_sync(0xffffffffu, w, 2);
     w |= __shfl_xor_sync(0xffffffffu, w, 4);
-    w |= __shfl_xor_sync(0xffffffffu, w, 8);
-    if (lane16 == 0) words[(rl & 31) * 4 + (rl >> 5)] = w;
-    if (r < M && col < K) {
-      const uint2 c = mx_encode8<F>(v[i], byte);
-      uint8_t* dst = data + r * rowb + (long)col * PER / 8;
+    if (row[i] < 0) break;
+    if (seg == 0) *reinterpret_cast<uint32_t*>(scales + mx_scale_word(row[i], tile[i], ktiles)) = w;
+    const int col = tile[i] * 128 + seg * 16;
+    if (row[i] < M && col < K) {
+      const uint2 lo = mx_encode8<F>(v, byte), hi = mx_encode8<F>(v + 8, byte);
+      const long at = (long)row[i] * K + col;
       if (F == MX_FP8)
-        *reinterpret_cast<uint2*>(dst) = c;
+        *reinterpret_cast<uint4*>(data + at) = make_uint4(lo.x, lo.y, hi.x, hi.y);
       else
-        *reinterpret_cast<uint32_t*>(dst) = c.x;
+        *reinterpret_cast<uint2*>(data + at / 2) = make_uint2(lo.x, hi.x);
     }
   }
-  __syncthreads();
-  if (threadIdx.x < 32)
-    reinterpret_cast<uint4*>(scales + (size_t)blockIdx.x * 512)[threadIdx.x] =
-        reinterpret_cast<const uint4*>(words)[threadIdx.x];
 }
 
 template <typename T, MxFormat F>
+cudaError_t launch_quantize(const void* x, long ldx, int M, int K, uint8_t* data, uint8_t* scales, cudaStream_t st) {
+  constexpr int QU = sizeof(T) == 2 ? 4 : 2;
+  const long ktiles = (K + 127) / 128, units = ((long)M + 127) / 128 * 32 * ktiles;
+  if (units > 0x7fffffffL) return cudaErrorInvalidValue;
+  constexpr int per = QT_THREADS / 32 * QU;
+  return launch_pdl(quantize_kernel<T, F, QU>, dim3((unsigned)((units + per - 1) / per)), dim3(QT_THREADS), 0, st,
+                    (const T*)x, ldx, M, K, (unsigned)ktiles, (unsigned)units, data, scales);
+}
+
+// ------------------------------------------------------------------ dequantise
+// One CTA per scale tile, 128 rows x 128 columns; sixteen lanes take a row, 8 values each.
+template <typename T, MxFormat F>
 __global__ void __launch_bounds__(QT_THREADS) dequantize_kernel(const uint8_t* __restrict__ data,
                                                                 const uint8_t* __restrict__ scales, int M, int K,
-                                                                T* __restrict__ out) {
+                                                                bool wide, T* __restrict__ out) {
   pdl_launch_dependents();
   pdl_wait();
   constexpr int PER = F == MX_FP8 ? 8 : 4;
@@ -110,24 +157,67 @@ __global__ void __launch_bounds__(QT_THREADS) dequantize_kernel(const uint8_t* _
         v[2 * p] = f.x;
         v[2 * p + 1] = f.y;
       }
-      store8(out + r * K + col, v);
+      store8w(out + r * K + col, v, wide);
     }
   }
 }
 
 // ------------------------------------------------------------------ residual + RMS norm
 // s = x + res, kept in x's type; y = s / sqrt(mean(s^2) + eps) * g + c on s as it is kept, with
-// g = a (plain gain) or 1 + a, and a, c the stream's own vectors. W warps share a row, which
-// stays in registers (NC chunks of 8 values per lane) between the sum of squares and the output:
-// x and res are read once, the sum and y written once, so bytes bound it. Four lanes make a
-// microscaled block. Rows past M up to the end of the last scale tile only zero their scales.
+// g = a (plain gain) or 1 + a, and a, c the stream's own vectors. W warps share a row, which stays
+// in registers (NC chunks of 8 values a lane) between the sum of squares and the output: x and res
+// are read once, the sum and y written once, so bytes bound it. A lane's loads are all in flight
+// together: they are predicated, not branched around, since a branch waits for its own. Four lanes
+// make a microscaled block. Rows past M up to the end of the last scale tile only get zero scales.
 enum NormOut { NO_F32 = 0, NO_BF16 = 1, NO_FP8 = 2, NO_FP4 = 3 };
 
+// A row's 1 / rms as r + lo: the reciprocal root is good to 2 steps, and a Newton step on its
+// residual, in the part that float32 would round away, keeps s * (r + lo) within about half a step
+// (left out where r^2 would overflow).
+__device__ __forceinline__ float2 inv_root(float m) {
+  const float r = rsqrtf(m), p = r * r, perr = fmaf(r, r, -p);
+  const float d = fmaf(-m, perr, fmaf(-m, p, 1.f));
+  return make_float2(r, m > 1e-30f && m < INFINITY ? 0.5f * r * d : 0.f);
+}
+
+// Eight consecutive values as they lie in memory, zeros where `in` is false: fp32 in one access
+// where `wide` says that they lie on 32 bytes
+template <typename T>
+struct Raw8 {
+  uint32_t w[2 * sizeof(T)];
+  __device__ __forceinline__ void load(const T* p, bool in, bool wide) {
+    if constexpr (sizeof(T) == 2) {
+      asm volatile(
+          "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+          "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+          "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+          : "=&r"(w[0]), "=&r"(w[1]), "=&r"(w[2]), "=&r"(w[3])
+          : "l"(p), "r"((int)in)
+          : "memory");
+    } else {
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %9, 0;\n\tsetp.ne.b32 q, %10, 0;\n\t"
+          "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+          "mov.b32 %4, 0;\n\tmov.b32 %5, 0;\n\tmov.b32 %6, 0;\n\tmov.b32 %7, 0;\n\t"
+          "@p ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+          "@q ld.global.v4.b32 {%0, %1, %2, %3}, [%8];\n\t"
+          "@q ld.global.v4.b32 {%4, %5, %6, %7}, [%8 + 16];\n\t}"
+          : "=&r"(w[0]), "=&r"(w[1]), "=&r"(w[2]), "=&r"(w[3]), "=&r"(w[4]), "=&r"(w[5]), "=&r"(w[6]), "=&r"(w[7])
+          : "l"(p), "r"((int)(in && wide)), "r"((int)(in && !wide))
+          : "memory");
+    }
+  }
+  __device__ __forceinline__ void unpack(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = __uint_as_float(sizeof(T) == 4 ? w[i] : i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+};
 template <typename TX, typename TR, int OUT, int W, int NC>
 __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
     add_rms_norm_kernel(const TX* x, const TR* res, TX* sum, const float* __restrict__ a,
                         const float* __restrict__ c, long bstride, int rows_per_batch, int M, int rows, int D,
-                        float eps, void* __restrict__ out, uint8_t* __restrict__ scales) {
+                        float eps, bool wide, void* __restrict__ out, uint8_t* __restrict__ scales) {
   pdl_launch_dependents();
   pdl_wait();
   constexpr int RPC = W == 1 ? 4 : 1;  // rows per CTA
@@ -144,31 +234,34 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
   }
   float v[NC][8];
   {
-    float r[NC][8];
+    Raw8<TX> xw[NC];
+    Raw8<TR> rw[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int ch = t + i * 32 * W;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = r[i][e] = 0.f;
-      if (ch < chunks) {
-        load8(x + row * D + ch * 8, v[i]);
-        load8(res + row * D + ch * 8, r[i]);
-      }
+      xw[i].load(x + row * D + ch * 8, ch < chunks, wide);
+      rw[i].load(res + row * D + ch * 8, ch < chunks, wide);
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int ch = t + i * 32 * W;
+      float r[8];
+      xw[i].unpack(v[i]);
+      rw[i].unpack(r);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = to_f(from_f<TX>(v[i][e] + r[i][e]));
-      if (ch < chunks) store8(sum + row * D + ch * 8, v[i]);
+      for (int e = 0; e < 8; ++e) v[i][e] = to_f(from_f<TX>(v[i][e] + r[e]));
+      if (ch < chunks) store8w(sum + row * D + ch * 8, v[i], wide);
     }
   }
-  float q = 0.f;
+  float2 q2 = make_float2(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < NC; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q = fmaf(v[i][e], v[i][e], q);
-  q = warp_sum(q);
+    for (int e = 0; e < 8; e += 2) {
+      const float2 s = make_float2(v[i][e], v[i][e + 1]);
+      q2 = fma2(s, s, q2);
+    }
+  float q = warp_sum(q2.x + q2.y);
   if constexpr (W > 1) {
     __shared__ float part[W];
     if (lane == 0) part[warp] = q;
@@ -177,44 +270,43 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
 #pragma unroll
     for (int w = 0; w < W; ++w) q += part[w];
   }
-  const float rstd = rsqrtf(q / (float)D + eps);
-  const long mb = (row / rows_per_batch) * bstride;
+  const float2 rstd = inv_root(q / (float)D + eps);
+  const float2 r2 = make_float2(rstd.x, rstd.x), lo2 = make_float2(rstd.y, rstd.y);
+  const long mb = ((int)row / rows_per_batch) * bstride;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int ch = t + i * 32 * W;
     const bool in = ch < chunks;
-    float y[8];
+    float y[8], g[8], h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = h[e] = 0.f;
     if (in) {
-      float g[8], h[8];
       load8(a + mb + ch * 8, g);
-      if (c) {
-        load8(c + mb + ch * 8, h);
+      if (c) load8(c + mb + ch * 8, h);
+    }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = v[i][e] * rstd * (1.f + g[e]) + h[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = v[i][e] * rstd * g[e];
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = 0.f;
+    for (int e = 0; e < 8; e += 2) {
+      const float2 s = make_float2(v[i][e], v[i][e + 1]), g2 = make_float2(g[e], g[e + 1]);
+      const float2 n = fma2(s, r2, mul2(s, lo2));
+      const float2 y2 = c ? add2(n, fma2(n, g2, make_float2(h[e], h[e + 1]))) : mul2(n, g2);
+      y[e] = y2.x;
+      y[e + 1] = y2.y;
     }
     if constexpr (OUT == NO_F32) {
-      if (in) store8(reinterpret_cast<float*>(out) + row * D + ch * 8, y);
+      if (in) store8w(reinterpret_cast<float*>(out) + row * D + ch * 8, y, wide);
     } else if constexpr (OUT == NO_BF16) {
-      if (in) store8(reinterpret_cast<bf16*>(out) + row * D + ch * 8, y);
+      if (in) store8w(reinterpret_cast<bf16*>(out) + row * D + ch * 8, y, wide);
     } else {
       constexpr MxFormat F = OUT == NO_FP8 ? MX_FP8 : MX_FP4;
-      uint32_t m = mx_amax8(y);
+      uint32_t m = mx_amax8(y);  // a block's four lanes are in the row or past it together
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const uint32_t byte = mx_scale_byte<F>(m);
-      uint32_t w = byte << (8 * ((lane >> 2) & 3));
+      uint32_t w = in ? byte << (8 * ((lane >> 2) & 3)) : 0u;
       w |= __shfl_xor_sync(0xffffffffu, w, 4);
       w |= __shfl_xor_sync(0xffffffffu, w, 8);
-      if ((lane & 15) == 0 && in)
-        *reinterpret_cast<uint32_t*>(scales + mx_scale_word(row, ch >> 4, ktiles)) = w;
       if (in) {
+        if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scales + mx_scale_word(row, ch >> 4, ktiles)) = w;
         const uint2 code = mx_encode8<F>(y, byte);
         if (F == MX_FP8)
           *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(out) + row * D + ch * 8) = code;
@@ -225,22 +317,34 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
   }
 }
 
+// Warps to a row and chunks to a lane, the first pair that the row fits. Measured: two or three
+// chunks a lane keep enough bytes in flight without starving the SM of warps (23040 x 1536 of fp32
+// and bf16: 66 us with 4 warps of 2, 75 with 1 of 6, 72 with 8 of 1); rows of bf16, half as many
+// bytes, want more chunks a lane (40 us with 2 of 3, 45 with 4 of 2); and of up to 256 rows each
+// is a latency (128 x 1536: 2.6 us with 8 of 1, 3.0 with 4 of 2).
 template <typename TX, typename TR, int OUT>
 cudaError_t launch_norm(const void* x, const void* res, void* sum, const float* a, const float* c, long bstride,
                         int rows_per_batch, int M, int D, float eps, void* out, uint8_t* scales, cudaStream_t st) {
   const int rows = OUT >= NO_FP8 ? (M + 127) / 128 * 128 : M;
   const int chunks = D / 8;
+  const bool wide = aligned32(x) && aligned32(res) && aligned32(sum) && aligned32(out);
 #define FH_NORM(WV, NCV)                                                                                             \
+  if (chunks <= 32 * WV * NCV)                                                                                        \
   return launch_pdl(add_rms_norm_kernel<TX, TR, OUT, WV, NCV>, dim3(WV == 1 ? (rows + 3) / 4 : rows),                 \
                     dim3(WV == 1 ? 128 : 32 * WV), 0, st, (const TX*)x, (const TR*)res, (TX*)sum, a, c, bstride,      \
-                    rows_per_batch, M, rows, D, eps, out, scales)
-  if (chunks <= 32 * 2) FH_NORM(1, 2);
-  if (chunks <= 32 * 4) FH_NORM(1, 4);
-  if (chunks <= 32 * 6) FH_NORM(1, 6);
-  if (chunks <= 32 * 8) FH_NORM(1, 8);
-  if (chunks <= 128 * 4) FH_NORM(4, 4);
-  if (chunks <= 256 * 4) FH_NORM(8, 4);
-  if (chunks <= 256 * 8) FH_NORM(8, 8);
+                    rows_per_batch, M, rows, D, eps, wide, out, scales)
+  FH_NORM(1, 1);
+  FH_NORM(1, 2);
+  if (M <= 256) FH_NORM(8, 1);
+  FH_NORM(2, 2);
+  if constexpr (sizeof(TX) == 2) FH_NORM(2, 3);
+  FH_NORM(4, 2);
+  if constexpr (sizeof(TX) == 2) FH_NORM(4, 4);
+  FH_NORM(8, 2);
+  FH_NORM(8, 3);
+  FH_NORM(8, 4);
+  FH_NORM(8, 6);
+  FH_NORM(8, 8);
 #undef FH_NORM
   return cudaErrorInvalidValue;
 }
@@ -265,17 +369,12 @@ cudaError_t norm_out(const void* x, const void* res, void* sum, const float* a, 
 
 cudaError_t mx_quantize(const void* x, long ldx, int M, int K, bool x_bf16, int fmt, void* data, void* scales,
                         cudaStream_t st) {
-  const long tiles = (long)((K + 127) / 128) * ((M + 127) / 128);
-  if (tiles > 0x7fffffffL) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)tiles);
   uint8_t *d = (uint8_t*)data, *s = (uint8_t*)scales;
   if (x_bf16)
-    return fmt == MX_FP8
-               ? launch_pdl(quantize_kernel<bf16, MX_FP8>, grid, dim3(QT_THREADS), 0, st, (const bf16*)x, ldx, M, K, d, s)
-               : launch_pdl(quantize_kernel<bf16, MX_FP4>, grid, dim3(QT_THREADS), 0, st, (const bf16*)x, ldx, M, K, d, s);
-  return fmt == MX_FP8
-             ? launch_pdl(quantize_kernel<float, MX_FP8>, grid, dim3(QT_THREADS), 0, st, (const float*)x, ldx, M, K, d, s)
-             : launch_pdl(quantize_kernel<float, MX_FP4>, grid, dim3(QT_THREADS), 0, st, (const float*)x, ldx, M, K, d, s);
+    return fmt == MX_FP8 ? launch_quantize<bf16, MX_FP8>(x, ldx, M, K, d, s, st)
+                         : launch_quantize<bf16, MX_FP4>(x, ldx, M, K, d, s, st);
+  return fmt == MX_FP8 ? launch_quantize<float, MX_FP8>(x, ldx, M, K, d, s, st)
+                       : launch_quantize<float, MX_FP4>(x, ldx, M, K, d, s, st);
 }
 
 cudaError_t mx_dequantize(const void* data, const void* scales, int M, int K, int fmt, void* out, bool out_bf16,
@@ -283,12 +382,13 @@ cudaError_t mx_dequantize(const void* data, const void* scales, int M, int K, in
   const long tiles = (long)((K + 127) / 128) * ((M + 127) / 128);
   if (tiles > 0x7fffffffL) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)tiles);
+  const bool wide = aligned32(out);
   const uint8_t *d = (const uint8_t*)data, *s = (const uint8_t*)scales;
   if (out_bf16)
-    return fmt == MX_FP8 ? launch_pdl(dequantize_kernel<bf16, MX_FP8>, grid, dim3(QT_THREADS), 0, st, d, s, M, K, (bf16*)out)
-                         : launch_pdl(dequantize_kernel<bf16, MX_FP4>, grid, dim3(QT_THREADS), 0, st, d, s, M, K, (bf16*)out);
-  return fmt == MX_FP8 ? launch_pdl(dequantize_kernel<float, MX_FP8>, grid, dim3(QT_THREADS), 0, st, d, s, M, K, (float*)out)
-                       : launch_pdl(dequantize_kernel<float, MX_FP4>, grid, dim3(QT_THREADS), 0, st, d, s, M, K, (float*)out);
+    return fmt == MX_FP8 ? launch_pdl(dequantize_kernel<bf16, MX_FP8>, grid, dim3(QT_THREADS), 0, st, d, s, M, K, wide, (bf16*)out)
+                         : launch_pdl(dequantize_kernel<bf16, MX_FP4>, grid, dim3(QT_THREADS), 0, st, d, s, M, K, wide, (bf16*)out);
+  return fmt == MX_FP8 ? launch_pdl(dequantize_kernel<float, MX_FP8>, grid, dim3(QT_THREADS), 0, st, d, s, M, K, wide, (float*)out)
+                       : launch_pdl(dequantize_kernel<float, MX_FP4>, grid, dim3(QT_THREADS), 0, st, d, s, M, K, wide, (float*)out);
 }
 
 cudaError_t add_rms_norm(const void* x, bool x_bf16, const void* res, bool res_bf16, void* sum, const float* a,
