@@ -196,6 +196,7 @@ struct MxParams {
   uint8_t* oscales;  // of a microscaled output
   int M, N, nk;      // nk: stages along K
   int last;          // MMAs of the last stage
+  int split;         // CTAs that share a tile
   int num_m, ntiles;
   int gelu;
   int tma;  // rows of out are 16-byte aligned: boxes leave by TMA
@@ -238,6 +239,22 @@ __device__ __forceinline__ uint4* box_unit(uint8_t* box, int row, int j) {
   return reinterpret_cast<uint4*>(box + row * RB + x * 16);
 }
 
+// A block of 32 values as codes, in 16-byte units at unit(0), unit(1) (e2m1: one); its scale byte
+template <MxFormat F, typename Unit>
+__device__ __forceinline__ uint32_t encode32(const float (&v)[32], Unit unit) {
+  const uint32_t byte = mx_scale_byte<F>(mx_amax32(v));
+  uint2 c[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c[j] = mx_encode8<F>(v + 8 * j, byte);
+  if constexpr (F == MX_FP8) {
+    *unit(0) = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
+    *unit(1) = make_uint4(c[2].x, c[2].y, c[3].x, c[3].y);
+  } else {
+    *unit(0) = make_uint4(c[0].x, c[1].x, c[2].x, c[3].x);
+  }
+  return byte;
+}
+
 // One row's 32 consecutive results into the warp's box, `c0` columns from its left; the block's
 // scale byte for microscaled ones.
 template <int OUT, int RB>
@@ -253,18 +270,8 @@ __device__ __forceinline__ uint32_t stage32(uint8_t* box, int row, int c0, const
     for (int j = 0; j < 4; ++j) store8(reinterpret_cast<bf16*>(box_unit<RB>(box, row, c0 / 8 + j)), v + 8 * j);
     return 0;
   } else {
-    constexpr MxFormat F = OUT == MXO_FP8 ? MX_FP8 : MX_FP4;
-    const uint32_t byte = mx_scale_byte<F>(mx_amax32(v));
-    uint2 c[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = mx_encode8<F>(v + 8 * j, byte);
-    if constexpr (F == MX_FP8) {
-      *box_unit<RB>(box, row, c0 / 16) = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
-      *box_unit<RB>(box, row, c0 / 16 + 1) = make_uint4(c[2].x, c[2].y, c[3].x, c[3].y);
-    } else {
-      *box_unit<RB>(box, row, c0 / 32) = make_uint4(c[0].x, c[1].x, c[2].x, c[3].x);
-    }
-    return byte;
+    return encode32<OUT == MXO_FP8 ? MX_FP8 : MX_FP4>(
+        v, [&](int j) { return box_unit<RB>(box, row, c0 / (OUT == MXO_FP8 ? 16 : 32) + j); });
   }
 }
 
@@ -281,6 +288,67 @@ __device__ __forceinline__ void copy_box(const MxParams& p, uint8_t* box, int ro
     for (int c = 0; c < COLS; c += 32)
       if (col + c + lane < p.N)
         dst[c + lane] = reinterpret_cast<const T*>(box_unit<RB>(box, r, (c + lane) / PER))[(c + lane) % PER];
+  }
+}
+
+// ---- a tile shared by the CTAs of a cluster (64 columns): each CTA owns 128 / parts of the rows and
+// takes all CTAs' sums of them in shared memory, [part][row][64], 16-byte units swizzled by the row.
+__device__ __forceinline__ uint32_t sum_unit(int part, int rows, int i, int unit) {
+  return (uint32_t)((part * rows + i) * 16 + (unit ^ (i & 15))) * 16u;
+}
+// Row r's columns 32 sub .. 32 sub + 32 to its owner
+__device__ __forceinline__ void send_row(const uint8_t* sums, int part, int rows, int r, int sub, const float (&v)[32]) {
+  const uint32_t to = mapa_shared(smem_u32(sums), (uint32_t)(r / rows));
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    st_cluster_v4(to + sum_unit(part, rows, r % rows, sub * 8 + j), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+// The owned rows, from global row `row0` on, of the tile at column n0: sums over the parts in their
+// order, a block of 32 columns a thread, and what follows them. `bias`: eight warps' columns.
+template <int OUT>
+__device__ __forceinline__ void join_rows(const MxParams& p, const uint8_t* sums, int parts, int row0, int n0,
+                                          const float4* bias) {
+  const int rows = 128 / parts;
+  if ((int)threadIdx.x >= 2 * rows) return;
+  const int i = threadIdx.x % rows, half = threadIdx.x / rows;
+  const int row = row0 + i, col = n0 + 32 * half;
+  const bool in = row < p.M && col < p.N;
+  uint32_t byte = 0;
+  if (in) {
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = 0.f;
+    for (int s = 0; s < parts; ++s) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float4 f = *reinterpret_cast<const float4*>(sums + sum_unit(s, rows, i, half * 8 + j));
+        v[4 * j] += f.x;
+        v[4 * j + 1] += f.y;
+        v[4 * j + 2] += f.z;
+        v[4 * j + 3] += f.w;
+      }
+    }
+    finish32(p, bias + half * 4 * (BIAS_BYTES / 16), v);
+    if constexpr (OUT == MXO_F32 || OUT == MXO_BF16) {
+      using T = typename std::conditional<OUT == MXO_F32, float, bf16>::type;
+      T* dst = reinterpret_cast<T*>(p.out) + (long)row * p.N + col;
+      if (p.tma && col + 32 <= p.N) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) store8(dst + j, v + j);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (col + j < p.N) dst[j] = from_f<T>(v[j]);
+      }
+    } else {
+      uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + ((long)row * p.N + col) / (OUT == MXO_FP8 ? 1 : 2);
+      byte = encode32<OUT == MXO_FP8 ? MX_FP8 : MX_FP4>(v, [&](int j) { return reinterpret_cast<uint4*>(dst) + j; });
+    }
+  }
+  if (OUT >= MXO_FP8) {  // 0 beyond the tensor, up to the end of its last scale tiles
+    const int okt = (p.N + 127) >> 7, blk = col >> 5;
+    if ((blk >> 2) < okt && row < ((p.M + 127) & ~127))
+      p.oscales[mx_scale_word(row, blk >> 2, okt) + (blk & 3)] = (uint8_t)byte;
   }
 }
 
@@ -346,7 +414,7 @@ __device__ __forceinline__ void issue_mma(int k, uint32_t d, uint64_t ad, uint64
                      sf + S::SFA_COLS + 4 * S::SFBT * atom + sfb_off, accumulate);
 }
 
-template <MxFormat F, int BN, bool PAIR, int OUT>
+template <MxFormat F, int BN, bool PAIR, int OUT, bool SPLIT>
 __global__ void __launch_bounds__(MXG_THREADS, 1)
     gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSW,
@@ -365,8 +433,13 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
-  const int cl = PAIR ? blockIdx.x >> 1 : blockIdx.x;
-  const int ncl = PAIR ? gridDim.x >> 1 : gridDim.x;
+  // SPLIT: the CTAs of a cluster share a tile, each a run of its stages, and join their sums below
+  const int parts = SPLIT ? p.split : 1;
+  const int part = SPLIT ? (int)cluster_ctarank() : 0;
+  const int cl = PAIR ? blockIdx.x >> 1 : blockIdx.x / parts;
+  const int ncl = PAIR ? gridDim.x >> 1 : gridDim.x / parts;
+  const int kb0 = SPLIT ? (int)((long)p.nk * part / parts) : 0;
+  const int kb1 = SPLIT ? (int)((long)p.nk * (part + 1) / parts) : p.nk;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::STAGES; ++s) {
@@ -397,8 +470,8 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
   }
   __syncwarp();
   tc_fence_before();
-  if constexpr (PAIR)
-    cluster_sync_all();  // both CTAs' barriers are initialised before any cross-CTA signal
+  if constexpr (PAIR || SPLIT)
+    cluster_sync_all();  // the cluster's CTAs run, with their barriers initialised, before any cross-CTA access
   else
     __syncthreads();
   tc_fence_after();
@@ -412,7 +485,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
     for (int tile = cl; ok && tile < p.ntiles; tile += ncl) {
       const int m0 = (tile % p.num_m) * S::TM + (int)rank * 128;
       const int n0 = (tile / p.num_m) * BN;
-      for (int kb = 0; kb < p.nk; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!warp_wait(&empty[cur.i], cur.phase ^ 1u, abort_flag, err)) {
           ok = false;
           break;
@@ -471,7 +544,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
         const uint32_t d_tmem = tmem_base + acc * S::ACC1;
         // the tile's first W row within its scale row tile (BN = 64, 192): 32 rows a column
         const uint32_t sfb_off = BN % 128 != 0 ? (uint32_t)((((tile / p.num_m) * BN) & 127) >> 5) : 0u;
-        for (int kb = 0; kb < p.nk; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if constexpr (S::NSF < S::STAGES) {
             if (pending == S::NSF) {
               ok = warp_wait(&empty[done.i], done.phase, abort_flag, err);
@@ -490,7 +563,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
             const uint32_t sf = tmem_base + S::SF_COL + sfi * S::SF_COLS;
             const uint64_t ad = ad0 + stage * (S::OPER_BYTES >> 4), bd = bd0 + stage * (S::OPER_BYTES >> 4);
             issue_scales<F, BN, PAIR>(sd0 + stage * (S::SF_BYTES >> 4), sf);
-            issue_mma<F, BN, PAIR>(0, d_tmem, ad, bd, sf, sfb_off, kb > 0);
+            issue_mma<F, BN, PAIR>(0, d_tmem, ad, bd, sf, sfb_off, kb > kb0);
             if (kb + 1 < p.nk || p.last == 4) {
 #pragma unroll
               for (int k = 1; k < 4; ++k) issue_mma<F, BN, PAIR>(k, d_tmem, ad, bd, sf, sfb_off, 1u);
@@ -499,7 +572,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
               if (p.last > 2) issue_mma<F, BN, PAIR>(2, d_tmem, ad, bd, sf, sfb_off, 1u);
             }
             commit<PAIR>(&empty[stage]);
-            if (kb + 1 == p.nk) commit<PAIR>(&tfull[acc]);
+            if (kb + 1 == kb1) commit<PAIR>(&tfull[acc]);
           }
           __syncwarp();
           if (++sf_next == S::NSF) sf_next = 0;
@@ -549,7 +622,13 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
       const int first = (S::OVERLAP != 0 && acc == 0) ? NCH / 2 : 0;  // chunk order: rotated for acc 0
       if (S::OVERLAP != 0 && !holds) release();
       uint32_t word = 0;
-      if (row0 < mpad) {
+      if constexpr (SPLIT) {
+        float v[32];
+        tmem_ld32(tb, v);
+        tc_wait_ld();
+        release();
+        if (row < p.M) send_row(smem + S::OUT_OFF, part, 128 / parts, quarter * 32 + lane, sub, v);
+      } else if (row0 < mpad) {
 #pragma unroll 1
         for (int i = 0; i < NCH; i += PER) {
           const int ch0 = S::OVERLAP != 0 ? (i + first) & (NCH - 1) : i;
@@ -610,7 +689,13 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
   // every role ends here with its warp converged again, so the barrier counts each warp once
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if constexpr (SPLIT) {
+    cluster_sync_all();  // all sums are here; nobody writes to this CTA any more
+    join_rows<OUT>(p, smem + S::OUT_OFF, parts, (cl % p.num_m) * S::TM + part * (128 / parts), (cl / p.num_m) * BN,
+                   reinterpret_cast<const float4*>(smem + S::OUT_OFF + 8 * BOX_BYTES));
+  } else {
+    __syncthreads();
+  }
   if (warp == 1) {
     if constexpr (PAIR) {
       // both CTAs are past their last TMEM access before the pair's allocation is released
@@ -622,13 +707,14 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
       tc_fence_after();
       tmem_dealloc_pair(tmem_base, S::TMEM_COLS);
     } else {
+      __syncwarp();
       tc_fence_after();
       tmem_dealloc(tmem_base, S::TMEM_COLS);
     }
   }
 }
 
-template <MxFormat F, int BN, bool PAIR, int OUT>
+template <MxFormat F, int BN, bool PAIR, int OUT, bool SPLIT>
 cudaError_t launch_mx(const MxMaps& maps, MxParams p, int K, int sms, cudaStream_t st) {
   using S = MxShape<F, BN, PAIR>;
   p.nk = (K + S::KB - 1) / S::KB;
@@ -639,10 +725,12 @@ cudaError_t launch_mx(const MxMaps& maps, MxParams p, int K, int sms, cudaStream
   const long tiles = (long)p.num_m * ((ncols + BN - 1) / BN);
   if (tiles > 0x7fffffffL) return cudaErrorInvalidValue;
   p.ntiles = (int)tiles;
-  const int slots = PAIR ? sms / 2 : sms;
+  const int cluster = PAIR ? 2 : SPLIT ? p.split : 1;
+  // a CTA that shares its tile takes no second one
+  const int slots = SPLIT ? (int)tiles : sms / cluster;
   const int grid = tiles < slots ? (int)tiles : slots;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(PAIR ? 2 * grid : grid);
+  cfg.gridDim = dim3(cluster * grid);
   cfg.blockDim = dim3(MXG_THREADS);
   cfg.dynamicSmemBytes = S::SMEM;
   cfg.stream = st;
@@ -650,35 +738,35 @@ cudaError_t launch_mx(const MxMaps& maps, MxParams p, int K, int sms, cudaStream
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemm_mx_kernel<F, BN, PAIR, OUT>, maps.a, maps.w, maps.sa, maps.sw, maps.o, p,
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, gemm_mx_kernel<F, BN, PAIR, OUT, SPLIT>, maps.a, maps.w, maps.sa, maps.sw, maps.o, p,
                             (unsigned*)nullptr);
 }
 
-template <MxFormat F, int BN, bool PAIR, int OUT>
-cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(gemm_mx_kernel<F, BN, PAIR, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)MxShape<F, BN, PAIR>::SMEM);
-}
-
-template <MxFormat F, int BN, bool PAIR>
+template <MxFormat F, int BN, bool PAIR, bool SPLIT>
 cudaError_t launch_out(const MxMaps& maps, const MxParams& p, int K, int out, int sms, cudaStream_t st) {
   switch (out) {
-    case MXO_F32: return launch_mx<F, BN, PAIR, MXO_F32>(maps, p, K, sms, st);
-    case MXO_BF16: return launch_mx<F, BN, PAIR, MXO_BF16>(maps, p, K, sms, st);
-    case MXO_FP8: return launch_mx<F, BN, PAIR, MXO_FP8>(maps, p, K, sms, st);
-    default: return launch_mx<F, BN, PAIR, MXO_FP4>(maps, p, K, sms, st);
+    case MXO_F32: return launch_mx<F, BN, PAIR, MXO_F32, SPLIT>(maps, p, K, sms, st);
+    case MXO_BF16: return launch_mx<F, BN, PAIR, MXO_BF16, SPLIT>(maps, p, K, sms, st);
+    case MXO_FP8: return launch_mx<F, BN, PAIR, MXO_FP8, SPLIT>(maps, p, K, sms, st);
+    default: return launch_mx<F, BN, PAIR, MXO_FP4, SPLIT>(maps, p, K, sms, st);
   }
 }
 
-template <MxFormat F, int BN, bool PAIR>
+template <MxFormat F, int BN, bool PAIR, int OUT, bool SPLIT>
+cudaError_t prepare_one() {
+  return cudaFuncSetAttribute(gemm_mx_kernel<F, BN, PAIR, OUT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)MxShape<F, BN, PAIR>::SMEM);
+}
+
+template <MxFormat F, int BN, bool PAIR, bool SPLIT>
 cudaError_t prepare_out() {
-  const cudaError_t es[] = {prepare_one<F, BN, PAIR, MXO_F32>(), prepare_one<F, BN, PAIR, MXO_BF16>(),
-                            prepare_one<F, BN, PAIR, MXO_FP8>(), prepare_one<F, BN, PAIR, MXO_FP4>()};
+  const cudaError_t es[] = {prepare_one<F, BN, PAIR, MXO_F32, SPLIT>(), prepare_one<F, BN, PAIR, MXO_BF16, SPLIT>(),
+                            prepare_one<F, BN, PAIR, MXO_FP8, SPLIT>(), prepare_one<F, BN, PAIR, MXO_FP4, SPLIT>()};
   for (cudaError_t e : es)
     if (e != cudaSuccess) return e;
   return cudaSuccess;
@@ -686,14 +774,15 @@ cudaError_t prepare_out() {
 
 }  // namespace
 
-// Every tile shape, for X(BN, PAIR)
-#define FH_MX_TILES(X) X(64, false) X(128, false) X(128, true) X(192, true) X(256, true)
+// Every tile shape, for X(BN, PAIR, SPLIT)
+#define FH_MX_TILES(X) \
+  X(64, false, true) X(64, false, false) X(128, false, false) X(128, true, false) X(192, true, false) X(256, true, false)
 
 cudaError_t gemm_mx_prepare() {
   cudaError_t e = cudaSuccess;
-#define FH_X(BNV, PAIRV)                                              \
-  if (e == cudaSuccess) e = prepare_out<MX_FP8, BNV, PAIRV>();        \
-  if (e == cudaSuccess) e = prepare_out<MX_FP4, BNV, PAIRV>();
+#define FH_X(BNV, PAIRV, SPLITV)                                       \
+  if (e == cudaSuccess) e = prepare_out<MX_FP8, BNV, PAIRV, SPLITV>(); \
+  if (e == cudaSuccess) e = prepare_out<MX_FP4, BNV, PAIRV, SPLITV>();
   FH_MX_TILES(FH_X)
 #undef FH_X
   return e;
@@ -704,16 +793,19 @@ cudaError_t gemm_mx_prepare() {
 // 4096 x 4096 x {4096 mxfp8, 8192 mxfp4}, 8640 x 4608 x 1536 mxfp8 and 23040 x 8960 x 1536 mxfp4
 // (us): wide tiles read fewer operand bytes per MMA and win where there are many rounds (the
 // last shape: 146 us at 256 columns on pairs, 159 at 128), narrow ones where a round of wide ones
-// would leave SMs idle (1280 x 1536 x 8960 mxfp4: 11.0 us at 128 columns, 14.4 at 256).
+// would leave SMs idle (1280 x 1536 x 8960 mxfp4: 11.0 us at 128 columns, 14.4 at 256). Where even
+// those leave most SMs idle, CTAs share a tile: joining their sums costs about 1.3 us (1 x 64 x 8960
+// mxfp8: 18.7 us on one CTA, 10.9, 7.5 and 5.5 on two, four and eight; 100 x 1536 x 8960: 18.9, 12.1
+// on two and 9.4 on four).
 MxTile gemm_mx_tile(int M, int N, int K, int fmt, int sms) {
   static const struct {
     MxTile t;
     float stage[2], fixed;
-  } shapes[] = {{{64, false}, {0.238f, 0.252f}, 0.33f},
-                {{128, false}, {0.270f, 0.283f}, 0.45f},
-                {{128, true}, {0.234f, 0.228f}, 0.52f},
-                {{192, true}, {0.281f, 0.324f}, 0.75f},
-                {{256, true}, {0.336f, 0.326f}, 1.45f}};
+  } shapes[] = {{{64, false, 1}, {0.238f, 0.252f}, 0.33f},
+                {{128, false, 1}, {0.270f, 0.283f}, 0.45f},
+                {{128, true, 1}, {0.234f, 0.228f}, 0.52f},
+                {{192, true, 1}, {0.281f, 0.324f}, 0.75f},
+                {{256, true, 1}, {0.336f, 0.326f}, 1.45f}};
   const int kb = fmt == MX_FP8 ? 128 : 256, nk = (K + kb - 1) / kb;
   MxTile best = shapes[0].t;
   float least = 0.f;
@@ -725,6 +817,14 @@ MxTile gemm_mx_tile(int M, int N, int K, int fmt, int sms) {
     if (least == 0.f || us < least) {
       least = us;
       best = s.t;
+    }
+  }
+  const long tiles = (long)((M + 127) / 128) * ((N + 127) / 128 * 2);
+  for (int split = 2; split <= 8; split *= 2) {
+    const float us = (float)((nk + split - 1) / split) * shapes[0].stage[fmt] + shapes[0].fixed + 1.3f;
+    if (split <= nk && tiles * split <= sms && us < least) {
+      least = us;
+      best = MxTile{64, false, split};
     }
   }
   return best;
@@ -742,10 +842,11 @@ cudaError_t gemm_mx(const MxMaps& maps, MxTile t, const float* bias, void* out, 
   p.N = N;
   p.gelu = gelu;
   p.tma = gemm_mx_tma_out(N, out_kind);
-#define FH_X(BNV, PAIRV)                                                                              \
-  if (t.bn == BNV && t.pair == PAIRV)                                                                 \
-    return fmt == MX_FP8 ? launch_out<MX_FP8, BNV, PAIRV>(maps, p, K, out_kind, sms, st)              \
-                         : launch_out<MX_FP4, BNV, PAIRV>(maps, p, K, out_kind, sms, st);
+  p.split = t.split;
+#define FH_X(BNV, PAIRV, SPLITV)                                                                      \
+  if (t.bn == BNV && t.pair == PAIRV && (t.split > 1) == SPLITV)                                      \
+    return fmt == MX_FP8 ? launch_out<MX_FP8, BNV, PAIRV, SPLITV>(maps, p, K, out_kind, sms, st)      \
+                         : launch_out<MX_FP4, BNV, PAIRV, SPLITV>(maps, p, K, out_kind, sms, st);
   FH_MX_TILES(FH_X)
 #undef FH_X
   return cudaErrorInvalidValue;

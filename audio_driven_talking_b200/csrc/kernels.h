@@ -152,6 +152,7 @@ struct MxMaps {
 struct MxTile {
   int bn;     // columns of a tile
   bool pair;  // 256-row tiles on CTA pairs, each loading half of the tile's W rows
+  int split;  // CTAs that share a tile, each a part of K (64-column tiles; else 1)
 };
 cudaError_t gemm_mx_prepare();
 MxTile gemm_mx_tile(int M, int N, int K, int fmt, int sms);

@@ -261,6 +261,15 @@ def test_linear_mx(M, N, K, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(1, 1, 8960), (1, 64, 8960), (1, 1536, 8960), (3, 200, 4096), (33, 96, 8960), (128, 160, 8960),
+                                   (129, 129, 8960), (200, 512, 8960), (300, 1000, 8960), (64, 4608, 8960), (17, 1056, 3008),
+                                   (250, 32, 16384), (1, 32, 1 << 18)])
+def test_linear_mx_few_rows_and_a_long_inner_dimension(M, N, K, fmt):
+    """Products whose few tiles are shared by clusters of two, four and eight CTAs."""
+    test_linear_mx(M, N, K, fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_linear_mx_scales_reach_the_right_blocks(fmt):
     """Operands of ones under scales that are different everywhere: sums of powers of two, exact."""
     M, N, K = 300, 270, 640
