@@ -171,8 +171,10 @@ __device__ __forceinline__ void gelu4(float* v) {
   for (int i = 0; i < 2; ++i) {
     asm("max.NaN.f32 %0, %1, 0fC0B33333;" : "=f"(x[i].x) : "f"(v[2 * i]));
     asm("max.NaN.f32 %0, %1, 0fC0B33333;" : "=f"(x[i].y) : "f"(v[2 * i + 1]));
+    // a NaN stays in its factor x and out of the shared reciprocal
+    const float2 w = make_float2(fmaxf(v[2 * i], -5.6f), fmaxf(v[2 * i + 1], -5.6f));
     const float2 k1 = make_float2(-2.3022082f, -2.3022082f), k3 = make_float2(-0.10294324f, -0.10294324f);
-    const float2 z = mul2(fma2(mul2(x[i], x[i]), k3, k1), x[i]);
+    const float2 z = mul2(fma2(mul2(w, w), k3, k1), w);
     float2 e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(z.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(z.y));

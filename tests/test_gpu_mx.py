@@ -295,6 +295,8 @@ def test_linear_mx_nan_blocks_stay_in_their_rows(fmt):
     nan = np.zeros((M, N), dtype=bool)
     nan[150], nan[:, 33] = True, True
     assert np.array_equal(np.isnan(y), nan)
+    g = f64(fh.linear_mx(fh.quantize(dev(x), fmt), fh.quantize(dev(w), fmt), act="gelu", out=F32))
+    assert np.array_equal(np.isnan(g), nan)
     q = fh.linear_mx(fh.quantize(dev(x), fmt), fh.quantize(dev(w), fmt), out="mxfp8")
     back = f64(fh.dequantize(q))
     assert np.isnan(back[150]).all() and np.isnan(back[:, 32:64]).all()
@@ -307,10 +309,18 @@ def test_linear_mx_gelu_tails():
     W = fh.quantize(torch.zeros(2048, 32, device="cuda"), "mxfp8")
     bias = torch.cat([torch.linspace(-12, 12, 2040, device="cuda"),
                       torch.tensor([-3e38, -1e20, -1e5, -50.0, 50.0, 1e5, 1e20, 3e38], device="cuda")])
+    inf = bias.clone()
+    inf[100], inf[201] = float("inf"), -float("inf")
+    far = f64(fh.linear_mx(A, W, inf, act="gelu", out=F32))[0]
+    assert far[100] == np.inf and abs(far[201]) < 2.0 ** -28
     got = f64(fh.linear_mx(A, W, bias, act="gelu", out=F32))[0]
     want = gelu64(f64(bias))
     # relative to x: the tanh form's own cancellation at the far negative end is not the kernel's
     assert np.isfinite(got).all()
+    # four neighbours share a reciprocal: what the infinities change in the others are its roundings, the
+    # three products into it, itself (2 u) and the three out of it, 8 u each way at most
+    rest = np.delete(np.arange(2048), [100, 201])
+    assert (np.abs(far - got)[rest] <= 16 * U * np.abs(got[rest])).all()
     assert (np.abs(got - want) <= 64 * U * np.abs(want) + 2 * U * np.abs(np.clip(f64(bias), -12, 12)) + U * np.abs(f64(bias)) * (f64(bias) > 0)).all()
 
 
