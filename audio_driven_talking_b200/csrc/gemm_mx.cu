@@ -200,6 +200,7 @@ struct MxParams {
   int last;          // MMAs of the last stage
   int split;         // CTAs that share a tile
   int num_m, ntiles;
+  int wide;  // 256-column tiles: those from here on are taken as two halves each
   int gelu;
   int tma;  // rows of out are 16-byte aligned: boxes leave by TMA
 };
@@ -354,6 +355,19 @@ __device__ __forceinline__ void join_rows(const MxParams& p, const uint8_t* sums
   }
 }
 
+// Where a tile lies, of the `ntiles` that are dealt out
+template <int BN>
+struct Tile {
+  int mt, n0;   // tile along M, first column
+  bool narrow;  // half of a 256-column tile
+  __device__ __forceinline__ Tile(const MxParams& p, int i) {
+    narrow = BN == 256 && i >= p.wide;
+    const int t = narrow ? p.wide + ((i - p.wide) >> 1) : i;
+    mt = t % p.num_m;
+    n0 = t / p.num_m * BN + (narrow && ((i - p.wide) & 1) ? BN / 2 : 0);
+  }
+};
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -407,12 +421,12 @@ __device__ __forceinline__ void issue_scales(uint64_t sd, uint32_t sf) {
 }
 template <MxFormat F, int BN, bool PAIR>
 __device__ __forceinline__ void issue_mma(int k, uint32_t d, uint64_t ad, uint64_t bd, uint32_t sf, uint32_t sfb_off,
-                                          uint32_t accumulate) {
+                                          uint32_t narrower, uint32_t accumulate) {
   using S = MxShape<F, BN, PAIR>;
   // 32 code bytes: 32 values (one block) of mxfp8, 64 values (two blocks) of mxfp4
   const int atom = F == MX_FP8 ? 0 : k >> 1;
   const int id = F == MX_FP8 ? k : 2 * (k & 1);
-  tc_mma_mx<F, PAIR>(d, ad + 2 * k, bd + 2 * k, idesc_mx(F, S::TM, BN, id), sf + 4 * atom,
+  tc_mma_mx<F, PAIR>(d, ad + 2 * k, bd + 2 * k, idesc_mx(F, S::TM, BN, id) - narrower, sf + 4 * atom,
                      sf + S::SFA_COLS + 4 * S::SFBT * atom + sfb_off, accumulate);
 }
 
@@ -485,8 +499,10 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
     int issues = 0;
     bool ok = true;
     for (int tile = cl; ok && tile < p.ntiles; tile += ncl) {
-      const int m0 = (tile % p.num_m) * S::TM + (int)rank * 128;
-      const int n0 = (tile / p.num_m) * BN;
+      const Tile<BN> at(p, tile);
+      const int m0 = at.mt * S::TM + (int)rank * 128;
+      // a narrow tile's box has W rows beyond it, which no MMA reads
+      const int w0 = at.n0 + (int)rank * (at.narrow ? S::WROWS / 2 : S::WROWS);
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!warp_wait(&empty[cur.i], cur.phase ^ 1u, abort_flag, err)) {
           ok = false;
@@ -497,9 +513,9 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
           uint8_t* sf = smem + S::SF_OFF + cur.i * S::SF_BYTES;
           if (rank == 0) mbar_expect_tx(&full[cur.i], S::TX_BYTES);
           load_codes<PAIR>(&tmA, &full[cur.i], sa, kb * 32, m0);
-          load_codes<PAIR>(&tmW, &full[cur.i], sa + S::A_BYTES, kb * 32, n0 + (int)rank * S::WROWS);
+          load_codes<PAIR>(&tmW, &full[cur.i], sa + S::A_BYTES, kb * 32, w0);
           load_scales<PAIR>(&tmSA, &full[cur.i], sf, kb * S::ATOMS, m0 >> 7);
-          load_scales<PAIR>(&tmSW, &full[cur.i], sf + S::SFA_BYTES, kb * S::ATOMS, n0 >> 7);
+          load_scales<PAIR>(&tmSW, &full[cur.i], sf + S::SFA_BYTES, kb * S::ATOMS, at.n0 >> 7);
         }
         __syncwarp();
         ++issues;
@@ -545,7 +561,9 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
         }
         const uint32_t d_tmem = tmem_base + acc * S::ACC1;
         // the tile's first W row within its scale row tile (BN = 64, 192): 32 rows a column
-        const uint32_t sfb_off = BN % 128 != 0 ? (uint32_t)((((tile / p.num_m) * BN) & 127) >> 5) : 0u;
+        const Tile<BN> at(p, tile);
+        const uint32_t sfb_off = BN % 128 != 0 ? (uint32_t)((at.n0 & 127) >> 5) : 0u;
+        const uint32_t narrower = at.narrow ? idesc_mx(F, S::TM, BN, 0) - idesc_mx(F, S::TM, BN / 2, 0) : 0u;
         for (int kb = kb0; kb < kb1; ++kb) {
           if constexpr (S::NSF < S::STAGES) {
             if (pending == S::NSF) {
@@ -565,13 +583,13 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
             const uint32_t sf = tmem_base + S::SF_COL + sfi * S::SF_COLS;
             const uint64_t ad = ad0 + stage * (S::OPER_BYTES >> 4), bd = bd0 + stage * (S::OPER_BYTES >> 4);
             issue_scales<F, BN, PAIR>(sd0 + stage * (S::SF_BYTES >> 4), sf);
-            issue_mma<F, BN, PAIR>(0, d_tmem, ad, bd, sf, sfb_off, kb > kb0);
+            issue_mma<F, BN, PAIR>(0, d_tmem, ad, bd, sf, sfb_off, narrower, kb > kb0);
             if (kb + 1 < p.nk || p.last == 4) {
 #pragma unroll
-              for (int k = 1; k < 4; ++k) issue_mma<F, BN, PAIR>(k, d_tmem, ad, bd, sf, sfb_off, 1u);
+              for (int k = 1; k < 4; ++k) issue_mma<F, BN, PAIR>(k, d_tmem, ad, bd, sf, sfb_off, narrower, 1u);
             } else {  // the last MMAs end with K: its padding meets at most the second block of one
-              if (p.last > 1) issue_mma<F, BN, PAIR>(1, d_tmem, ad, bd, sf, sfb_off, 1u);
-              if (p.last > 2) issue_mma<F, BN, PAIR>(2, d_tmem, ad, bd, sf, sfb_off, 1u);
+              if (p.last > 1) issue_mma<F, BN, PAIR>(1, d_tmem, ad, bd, sf, sfb_off, narrower, 1u);
+              if (p.last > 2) issue_mma<F, BN, PAIR>(2, d_tmem, ad, bd, sf, sfb_off, narrower, 1u);
             }
             commit<PAIR>(&empty[stage]);
             if (kb + 1 == kb1) commit<PAIR>(&tfull[acc]);
@@ -602,14 +620,16 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
     int local = 0;
     for (int tile = cl; tile < p.ntiles; tile += ncl, ++local) {
       const int acc = local & 1;
-      const int m0 = (tile % p.num_m) * S::TM + (int)rank * 128;
-      const int n0 = (tile / p.num_m) * BN + sub * HALF;
-      if (lane < HALF / 4) bias[lane] = load_bias(p, n0 + 4 * lane);  // while the MMAs run
+      const Tile<BN> at(p, tile);
+      const int m0 = at.mt * S::TM + (int)rank * 128;
+      const int share = at.narrow ? HALF / 2 : HALF, nch = share / 32;
+      const int n0 = at.n0 + sub * share;
+      if (lane < share / 4) bias[lane] = load_bias(p, n0 + 4 * lane);  // while the MMAs run
       __syncwarp();
       const int row0 = m0 + quarter * 32, row = row0 + lane;
       if (!warp_wait(&tfull[acc], (local >> 1) & 1, abort_flag, err)) break;  // tcgen05.ld is warp-collective
       tc_fence_after();
-      const uint32_t tb = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * S::ACC1 + sub * HALF;
+      const uint32_t tb = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * S::ACC1 + sub * share;
       auto release = [&]() {
         tc_fence_before();
         if constexpr (PAIR)
@@ -620,9 +640,11 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
       // At BN = 256 the accumulators share columns 192-255: the last 64 of the first, the first
       // 64 of the second. The warps that hold them read them first and release them, so that the
       // next tile's MMAs run under the rest of this epilogue.
-      const bool holds = S::OVERLAP != 0 && sub == (acc ^ 1);
-      const int first = (S::OVERLAP != 0 && acc == 0) ? NCH / 2 : 0;  // chunk order: rotated for acc 0
-      if (S::OVERLAP != 0 && !holds) release();
+      // (A narrow tile is a CTA's last.)
+      const bool overlaps = S::OVERLAP != 0 && !at.narrow;
+      const bool holds = overlaps && sub == (acc ^ 1);
+      const int first = overlaps && acc == 0 ? NCH / 2 : 0;  // chunk order: rotated for acc 0
+      if (overlaps && !holds) release();
       uint32_t word = 0;
       if constexpr (SPLIT) {
         float v[32];
@@ -632,7 +654,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
         if (row < p.M) send_row(smem + S::OUT_OFF, part, 128 / parts, quarter * 32 + lane, sub, v);
       } else if (row0 < mpad) {
 #pragma unroll 1
-        for (int i = 0; i < NCH; i += PER) {
+        for (int i = 0; i < nch; i += PER) {
           const int ch0 = S::OVERLAP != 0 ? (i + first) & (NCH - 1) : i;
           const int col = n0 + ch0 * 32;
           float v[PER][32];
@@ -640,7 +662,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
           for (int k = 0; k < PER; ++k) tmem_ld32(tb + (ch0 + k) * 32, v[k]);
           tc_wait_ld();
           if (holds && i + PER == NCH / 2) release();
-          if (S::OVERLAP == 0 && i + PER == NCH) release();
+          if (!overlaps && i + PER == nch) release();
           if (col >= p.N || row0 >= p.M) continue;  // nothing of the tensor
 #pragma unroll
           for (int k = 0; k < PER; ++k) finish32(p, bias + (ch0 + k) * 8, v[k]);
@@ -674,12 +696,12 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
             }
           } else if ((n0 >> 7) < okt) {  // scales of this warp's columns; 0 beyond the tensor
             uint8_t* dst = p.oscales + mx_scale_word(row, n0 >> 7, okt) + ((n0 >> 5) & 3);
-            if constexpr (NCH == 4) *reinterpret_cast<uint32_t*>(dst) = word;
-            if constexpr (NCH == 2) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)word;
-            if constexpr (NCH == 1) *dst = (uint8_t)word;
+            if (NCH == 4 && nch == 4) *reinterpret_cast<uint32_t*>(dst) = word;
+            if (NCH == 2 || (NCH == 4 && nch == 2)) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)word;
+            if (NCH == 1) *dst = (uint8_t)word;
           }
         }
-      } else if (S::OVERLAP == 0 || holds) {
+      } else if (!overlaps || holds) {
         release();
       }
       __syncwarp();  // the bias is read
@@ -716,6 +738,13 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
   }
 }
 
+// Of the 256-column tiles, those taken whole: where the last round would leave half of the CTA
+// pairs idle, its tiles are taken as halves.
+int wide_tiles(long tiles, int slots) {
+  const long rest = tiles % slots;
+  return (int)(2 * rest <= slots ? tiles - rest : tiles);
+}
+
 template <MxFormat F, int BN, bool PAIR, int OUT, bool SPLIT>
 cudaError_t launch_mx(const MxMaps& maps, MxParams p, int K, int sms, cudaStream_t st) {
   using S = MxShape<F, BN, PAIR>;
@@ -725,12 +754,13 @@ cudaError_t launch_mx(const MxMaps& maps, MxParams p, int K, int sms, cudaStream
   // a microscaled output's scale tiles are written whole: tiles up to the next multiple of 128
   const int ncols = OUT >= MXO_FP8 ? (p.N + 127) / 128 * 128 : p.N;
   const long tiles = (long)p.num_m * ((ncols + BN - 1) / BN);
-  if (tiles > 0x7fffffffL) return cudaErrorInvalidValue;
-  p.ntiles = (int)tiles;
+  if (tiles > 0x3fffffffL) return cudaErrorInvalidValue;
   const int cluster = PAIR ? 2 : SPLIT ? p.split : 1;
   // a CTA that shares its tile takes no second one
   const int slots = SPLIT ? (int)tiles : sms / cluster;
-  const int grid = tiles < slots ? (int)tiles : slots;
+  p.wide = BN == 256 ? wide_tiles(tiles, slots) : (int)tiles;
+  p.ntiles = p.wide + 2 * ((int)tiles - p.wide);
+  const int grid = p.ntiles < slots ? p.ntiles : slots;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster * grid);
   cfg.blockDim = dim3(MXG_THREADS);
@@ -815,7 +845,9 @@ MxTile gemm_mx_tile(int M, int N, int K, int fmt, int sms) {
     const int tm = s.t.pair ? 256 : 128, slots = s.t.pair ? sms / 2 : sms;
     if (slots < 1) continue;
     const long tiles = (long)((M + tm - 1) / tm) * ((N + s.t.bn - 1) / s.t.bn);
-    const float us = (float)((tiles + slots - 1) / slots) * (nk * s.stage[fmt] + s.fixed);
+    float us = (float)((tiles + slots - 1) / slots) * (nk * s.stage[fmt] + s.fixed);
+    if (s.t.bn == 256 && wide_tiles(tiles, slots) < tiles)  // the last round is one of 128 columns
+      us = (float)(tiles / slots) * (nk * s.stage[fmt] + s.fixed) + nk * shapes[2].stage[fmt] + shapes[2].fixed;
     if (least == 0.f || us < least) {
       least = us;
       best = s.t;

@@ -270,6 +270,16 @@ def test_linear_mx_few_rows_and_a_long_inner_dimension(M, N, K, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(4096, 4096, 1536), (4097, 4224, 2080), (2500, 8961, 1536), (3900, 8960, 1568), (8640, 1536, 4096)])
+def test_linear_mx_wide_tiles(M, N, K, fmt):
+    """Several rounds of 256-column tiles, the last one of halves, on ragged edges."""
+    A, W, bias = operands(M + N + K, M, N, K, fmt)
+    y, tol = linear_reference(A, W, bias, "gelu")
+    for out in (BF, F32, "mxfp8", "mxfp4") if N % 32 == 0 else (BF, F32):
+        check_any(fh.linear_mx(A, W, bias, act="gelu", out=out), y, tol)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_linear_mx_scales_reach_the_right_blocks(fmt):
     """Operands of ones under scales that are different everywhere: sums of powers of two, exact."""
     M, N, K = 300, 270, 640
