@@ -826,9 +826,10 @@ cudaError_t gemm_mx_prepare() {
 // (us): wide tiles read fewer operand bytes per MMA and win where there are many rounds (the
 // last shape: 146 us at 256 columns on pairs, 159 at 128), narrow ones where a round of wide ones
 // would leave SMs idle (1280 x 1536 x 8960 mxfp4: 11.0 us at 128 columns, 14.4 at 256). Where even
-// those leave most SMs idle, CTAs share a tile: joining their sums costs about 1.3 us (1 x 64 x 8960
-// mxfp8: 18.7 us on one CTA, 10.9, 7.5 and 5.5 on two, four and eight; 100 x 1536 x 8960: 18.9, 12.1
-// on two and 9.4 on four).
+// those leave most SMs idle, CTAs share a tile, which costs them 2.5 us, 3.5 where eight of one GPC
+// have to start together (1 x 64 x 8960 mxfp8: 18.7 us on one CTA, 10.9, 7.5 and 5.5 on two, four
+// and eight; 100 x 1536 x 8960: 18.9, 12.1 on two and 9.4 on four; but 437 x 1008 x 1568 5.8 on one
+// and 6.9 on two, and 100 x 1000 x 2048 mxfp4 4.5 on one and 10.3 on eight, 128 CTAs in all).
 MxTile gemm_mx_tile(int M, int N, int K, int fmt, int sms) {
   static const struct {
     MxTile t;
@@ -855,8 +856,8 @@ MxTile gemm_mx_tile(int M, int N, int K, int fmt, int sms) {
   }
   const long tiles = (long)((M + 127) / 128) * ((N + 127) / 128 * 2);
   for (int split = 2; split <= 8; split *= 2) {
-    const float us = (float)((nk + split - 1) / split) * shapes[0].stage[fmt] + shapes[0].fixed + 1.3f;
-    if (split <= nk && tiles * split <= sms && us < least) {
+    const float us = (float)((nk + split - 1) / split) * shapes[0].stage[fmt] + shapes[0].fixed + (split == 8 ? 3.5f : 2.5f);
+    if (split <= nk && tiles * split <= (split == 8 ? sms / 2 : sms) && us < least) {
       least = us;
       best = MxTile{64, false, split};
     }
