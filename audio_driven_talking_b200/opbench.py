@@ -5,6 +5,9 @@ for ncu captures of one kernel on a case of a chosen size.
     python -m audio_driven_talking_b200.opbench attention --tokens 1280
     python -m audio_driven_talking_b200.opbench linear --m 1280 --n 1536 --k 1536
     python -m audio_driven_talking_b200.opbench cross_attention --tokens 1280
+    python -m audio_driven_talking_b200.opbench quantize --m 8640 --k 8960 --format mxfp8
+    python -m audio_driven_talking_b200.opbench add_rms_norm --rows 23040 --out mxfp8
+    python -m audio_driven_talking_b200.opbench linear_mx --m 8640 --n 4608 --k 1536 --format mxfp8 [--act gelu]
     python -m audio_driven_talking_b200.opbench slice --blocks 2 --iters 3 [--renoise]
     python -m audio_driven_talking_b200.opbench slice_kernels --blocks 30
 
@@ -114,6 +117,54 @@ def cross_attention(a):
             "us": us, "bytes": nbytes, "gb_per_s": nbytes / us / 1e3}
 
 
+def _out(name):
+    import torch
+    return {"bf16": torch.bfloat16, "f32": torch.float32}.get(name, name)
+
+
+def _mx_bytes(rows, cols, kind):
+    """Bytes of a rows x cols tensor: fp32, bf16 or microscaled with its scales."""
+    if kind in ("f32", "bf16"):
+        return rows * cols * (4 if kind == "f32" else 2)
+    return rows * cols // (1 if kind == "mxfp8" else 2) + rows * cols // 32
+
+
+def quantize(a):
+    import torch
+    x = torch.randn((a.m, a.k), device="cuda", generator=_gen(6)).to(torch.bfloat16)
+    us = _time(lambda: fh.quantize(x, a.format), a.iters, a.warmup)
+    nbytes = _mx_bytes(a.m, a.k, "bf16") + _mx_bytes(a.m, a.k, a.format)
+    return {"op": "quantize", "kernel": "quantize_kernel", "rows": a.m, "cols": a.k, "format": a.format, "us": us,
+            "bytes": nbytes, "gb_per_s": nbytes / us / 1e3}
+
+
+def add_rms_norm(a):
+    """fp32 rows and a bf16 branch, with one stream's scale and shift, as before a block's projection."""
+    import torch
+    g = _gen(7)
+    M, D = a.rows, a.dim
+    x = torch.randn((M, D), device="cuda", generator=g)
+    r = torch.randn((M, D), device="cuda", generator=g).to(torch.bfloat16)
+    sc, sh = (0.1 * torch.randn((D,), device="cuda", generator=g) for _ in range(2))
+    us = _time(lambda: fh.add_rms_norm(x, r, sc, sh, out=_out(a.out)), a.iters, a.warmup)
+    nbytes = M * D * (4 + 2 + 4) + _mx_bytes(M, D, a.out)
+    return {"op": "add_rms_norm", "kernel": "add_rms_norm_kernel", "rows": M, "dim": D, "out": a.out, "us": us,
+            "bytes": nbytes, "gb_per_s": nbytes / us / 1e3}
+
+
+def linear_mx(a):
+    import torch
+    g = _gen(8)
+    M, N, K = a.m, a.n, a.k
+    A = fh.quantize(torch.randn((M, K), device="cuda", generator=g), a.format)
+    W = fh.quantize(torch.randn((N, K), device="cuda", generator=g) / math.sqrt(K), a.format)
+    b = torch.randn((N,), device="cuda", generator=g)
+    us = _time(lambda: fh.linear_mx(A, W, b, act=a.act, out=_out(a.out)), a.iters, a.warmup)
+    flops = 2.0 * M * N * K
+    return {"op": "linear_mx", "kernel": "gemm_mx_kernel", "m": M, "n": N, "k": K, "format": a.format, "act": a.act,
+            "out": a.out, "us": us, "flop": flops, "tflop_per_s": flops / us / 1e6}
+
+
 def slice_(a):
     """The whole sampler on a model of `blocks` blocks (the kernels of the 30-block model on a
     small device footprint): one launch each of the small per-step kernels per step."""
@@ -178,7 +229,8 @@ def slice_kernels(a):
 
 def parser():
     p = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
-    p.add_argument("op", choices=["row_norm", "attention", "linear", "cross_attention", "slice", "slice_kernels"])
+    p.add_argument("op", choices=["row_norm", "attention", "linear", "cross_attention", "quantize", "add_rms_norm", "linear_mx",
+                                  "slice", "slice_kernels"])
     p.add_argument("--rows", type=int, default=65536)
     p.add_argument("--dim", type=int, default=1536)
     p.add_argument("--mode", type=int, default=0)
@@ -189,6 +241,9 @@ def parser():
     p.add_argument("--m", type=int, default=1280)
     p.add_argument("--n", type=int, default=1536)
     p.add_argument("--k", type=int, default=1536)
+    p.add_argument("--format", choices=["mxfp8", "mxfp4"], default="mxfp8", help="of microscaled operands")
+    p.add_argument("--out", choices=["bf16", "f32", "mxfp8", "mxfp4"], default="bf16")
+    p.add_argument("--act", choices=["gelu"], default=None)
     p.add_argument("--blocks", type=int, default=2)
     p.add_argument("--renoise", action="store_true")
     p.add_argument("--iters", type=int, default=20)
@@ -204,7 +259,8 @@ def main(argv=None):
     import torch
     torch.cuda.set_device(0)
     fn = {"row_norm": row_norm, "attention": attention, "linear": linear, "cross_attention": cross_attention,
-          "slice": slice_, "slice_kernels": slice_kernels}[a.op]
+          "quantize": quantize, "add_rms_norm": add_rms_norm, "linear_mx": linear_mx, "slice": slice_,
+          "slice_kernels": slice_kernels}[a.op]
     r = fn(a)
     r["graph"] = GRAPH
     print(json.dumps(r))
