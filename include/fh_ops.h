@@ -106,7 +106,7 @@ enum fh_act { FH_ACT_NONE = 0, FH_ACT_GELU = 1 };
 
 /* out [M][N] = act(A [M][K] * W [N][K]^T + bias [N]) of two microscaled operands of one type, on
  * the block-scaled tensor core, accumulated in fp32; bias float32 or null; act FH_ACT_GELU: the
- * tanh form of GELU. K % 32 == 0; N any, but a multiple of 32 for a microscaled out. out_type any
+ * tanh form of GELU (results for arguments below -5.6 are off by up to 3e-9). K % 32 == 0; N any, but a multiple of 32 for a microscaled out. out_type any
  * of fh_dtype; out_scales for the microscaled ones, else null. A row or column with a NaN scale
  * gives NaN results. out may not overlap the operands. */
 int fh_op_linear_mx(const void* A, const void* A_scales, const void* W, const void* W_scales, const float* bias,

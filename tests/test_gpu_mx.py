@@ -188,6 +188,32 @@ def test_add_rms_norm_in_place_and_zero_rows():
         fh.add_rms_norm(big[:50], res, g, sum_out=big[1:])
 
 
+@pytest.mark.parametrize("D", [64, 1536, 3104, 8224])
+def test_add_rms_norm_on_16_byte_boundaries(D):
+    """Inputs, sum and vectors that lie on 16 bytes but not on 32."""
+    M = 37
+
+    def off(a, dtype=F32):
+        t = dev(a, dtype)
+        skip = 16 // t.element_size()
+        buf = torch.empty(t.numel() + skip, dtype=dtype, device="cuda")
+        buf[skip:] = t.reshape(-1)
+        v = buf[skip:].view(t.shape)
+        assert v.data_ptr() % 32 == 16
+        return v
+
+    for xt, rt in ((F32, BF), (BF, F32), (F32, F32)):
+        x, res, a, c = randn(D, M, D), randn(D + 1, M, D), 0.3 * randn(D + 2, D), randn(D + 3, D)
+        want = fh.add_rms_norm(dev(x, xt), dev(res, rt), dev(a), dev(c), out="mxfp8")
+        total = off(np.zeros((M, D)), xt)
+        got = fh.add_rms_norm(off(x, xt), off(res, rt), off(a), off(c), out="mxfp8", sum_out=total)
+        assert torch.equal(got[0], want[0])
+        assert torch.equal(got[1].data, want[1].data) and torch.equal(got[1].scales, want[1].scales)
+    q = fh.quantize(off(randn(D, M, D)), "mxfp4")
+    p = fh.quantize(dev(randn(D, M, D)), "mxfp4")
+    assert torch.equal(q.data, p.data) and torch.equal(q.scales, p.scales)
+
+
 def test_add_rms_norm_rows_that_are_not_finite():
     x, res = dev(randn(1, 9, 256)), dev(randn(2, 9, 256), BF)
     x[2, 5], res[6, 200] = float("inf"), float("nan")
@@ -267,6 +293,17 @@ def test_linear_mx(M, N, K, fmt):
 def test_linear_mx_few_rows_and_a_long_inner_dimension(M, N, K, fmt):
     """Products whose few tiles are shared by clusters of two, four and eight CTAs."""
     test_linear_mx(M, N, K, fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("N", [1, 2, 4, 7, 8, 12, 16, 24, 31, 40, 63, 65, 72, 100, 120, 127, 136])
+def test_linear_mx_narrow_results(N, fmt):
+    """Rows of results shorter than a box, on and off 16-byte boundaries, in both float types."""
+    for M, K in ((3, 64), (130, 1024), (5, 8960)):
+        A, W, bias = operands(N + K, M, N, K, fmt)
+        y, tol = linear_reference(A, W, bias, "gelu")
+        for out in (BF, F32):
+            check_values(fh.linear_mx(A, W, bias, act="gelu", out=out), y, tol)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -479,6 +516,50 @@ def test_other_streams():
     back = fh.dequantize(q, stream=torch.cuda.default_stream())
     torch.cuda.synchronize()
     assert torch.equal(back, fh.dequantize(fh.quantize(x, "mxfp4")))
+
+
+def test_calls_from_several_threads():
+    """Threads with streams of their own, at once: checks, allocations and launches share nothing."""
+    import threading
+    ins = [ff_inputs(s, 200, 384, 1024, "mxfp8") for s in range(41, 45)]
+    want = [[t.clone() for t in flat(feed_forward(*i, "mxfp8", BF))] for i in ins]
+    torch.cuda.synchronize()
+    good = [False] * len(ins)
+
+    def work(k):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            good[k] = all(torch.equal(a, b) for _ in range(10)
+                          for a, b in zip(flat(feed_forward(*ins[k], "mxfp8", BF)), want[k]))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(ins))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(good)
+
+
+def test_first_call_inside_a_capture():
+    """Nothing that the first calls set up is forbidden while a stream captures: a fresh process, whose
+    first calls are recorded and replayed."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = (
+        "import torch, audio_driven_talking_b200 as fh\n"
+        "x = torch.randn(64, 256, device='cuda'); g = torch.ones(256, device='cuda'); torch.cuda.synchronize()\n"
+        "def run():\n"
+        "    s, h = fh.add_rms_norm(x, x, g)\n"
+        "    y = fh.linear_mx(h, h, out='mxfp4')\n"
+        "    return [s, h.data, y.data, fh.dequantize(y), fh.quantize(x).data]\n"
+        "graph = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(graph): got = run()\n"
+        "graph.replay(); torch.cuda.synchronize()\n"
+        "assert all(torch.equal(a, b) for a, b in zip(got, run()))\n"
+        "print('equal')\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "equal" in r.stdout, r.stderr[-2000:]
 
 
 @pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two devices")
