@@ -661,7 +661,6 @@ int prepare_device(int dev) {
   if (e == cudaSuccess) e = attn_tc_prepare();
   if (e == cudaSuccess) e = cross_attn_prepare();
   if (e == cudaSuccess) e = xattn_tc_prepare();
-  if (e == cudaSuccess) e = gemm_mx_prepare();
   if (e != cudaSuccess) return fail(FH_ERR_CUDA, "kernel attribute setup: %s", cudaGetErrorString(e));
   g_prepared[dev] = true;
   return FH_OK;
@@ -1451,7 +1450,6 @@ int fh_op_linear_mx(const void* A, const void* A_scales, const void* W, const vo
   if (!load_encode()) return fail(FH_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled unavailable");
   int dev = 0, sms = 148;
   CK(cudaGetDevice(&dev));
-  RUN(prepare_device(dev));
   CK(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   const MxTile t = gemm_mx_tile(M, N, K, mx_fmt(mxtype), sms);
   const uint64_t pitch = mxtype == FH_MXFP4 ? K / 2 : K;

@@ -13,12 +13,15 @@
 //              GELU, and fp32 or bf16 rows, or the microscaled form again: a thread holds 32
 //              consecutive values of a row, which is a block. Results leave by TMA from boxes
 //              in shared memory.
+// CTAs take tiles in rounds, alone or as pairs (cta_group::2, each loading half of the W tile); or
+// the CTAs of a cluster share one tile's stages and join their sums in shared memory.
 // Warps 0 and 1 run their loops whole and elect a lane to issue: with one lane in a divergent
 // branch instead, issuing a stage's four MMAs took longer than running them (4096^3 mxfp8: 78.8 us
 // against 59.3). What bounds the loop now is shared memory: a stage's 32 KB are written by TMA and
 // read by the MMAs at 128 bytes a clock each SM, 512 of the about 600 clocks that a stage of a
 // 256 x 256 tile takes.
 // Every wait is bounded (FH_WAIT_LIMIT_NS), as in gemm_tc.cu.
+#include <atomic>
 #include <type_traits>
 
 #include "kernels.h"
@@ -405,8 +408,9 @@ struct Ring {
   }
 };
 
-// The scale copies and the MMAs (NMMA of 4) of one stage; `ad`, `bd`, `sd` describe its operands
-// and its scale tiles in shared memory, `sf` its scale buffer in TMEM.
+// The scale copies and the k-th of the four MMAs of a stage; `ad`, `bd`, `sd` describe its operands
+// and its scale tiles in shared memory, `sf` its scale buffer in TMEM; `narrower`: what the
+// instruction descriptor of a narrow tile is less.
 template <MxFormat F, int BN, bool PAIR>
 __device__ __forceinline__ void issue_scales(uint64_t sd, uint32_t sf) {
   using S = MxShape<F, BN, PAIR>;
@@ -761,6 +765,17 @@ cudaError_t launch_mx(const MxMaps& maps, MxParams p, int K, int sms, cudaStream
   p.wide = BN == 256 ? wide_tiles(tiles, slots) : (int)tiles;
   p.ntiles = p.wide + 2 * ((int)tiles - p.wide);
   const int grid = p.ntiles < slots ? p.ntiles : slots;
+  // the kernel's shared memory, once on each device; only kernels in use are loaded
+  static std::atomic<uint64_t> prepared{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (e == cudaSuccess && !(prepared.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(gemm_mx_kernel<F, BN, PAIR, OUT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)S::SMEM);
+    if (e == cudaSuccess) prepared.fetch_or(bit, std::memory_order_relaxed);
+  }
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster * grid);
   cfg.blockDim = dim3(MXG_THREADS);
@@ -789,36 +804,11 @@ cudaError_t launch_out(const MxMaps& maps, const MxParams& p, int K, int out, in
   }
 }
 
-template <MxFormat F, int BN, bool PAIR, int OUT, bool SPLIT>
-cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(gemm_mx_kernel<F, BN, PAIR, OUT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)MxShape<F, BN, PAIR>::SMEM);
-}
-
-template <MxFormat F, int BN, bool PAIR, bool SPLIT>
-cudaError_t prepare_out() {
-  const cudaError_t es[] = {prepare_one<F, BN, PAIR, MXO_F32, SPLIT>(), prepare_one<F, BN, PAIR, MXO_BF16, SPLIT>(),
-                            prepare_one<F, BN, PAIR, MXO_FP8, SPLIT>(), prepare_one<F, BN, PAIR, MXO_FP4, SPLIT>()};
-  for (cudaError_t e : es)
-    if (e != cudaSuccess) return e;
-  return cudaSuccess;
-}
-
 }  // namespace
 
 // Every tile shape, for X(BN, PAIR, SPLIT)
 #define FH_MX_TILES(X) \
   X(64, false, true) X(64, false, false) X(128, false, false) X(128, true, false) X(192, true, false) X(256, true, false)
-
-cudaError_t gemm_mx_prepare() {
-  cudaError_t e = cudaSuccess;
-#define FH_X(BNV, PAIRV, SPLITV)                                       \
-  if (e == cudaSuccess) e = prepare_out<MX_FP8, BNV, PAIRV, SPLITV>(); \
-  if (e == cudaSuccess) e = prepare_out<MX_FP4, BNV, PAIRV, SPLITV>();
-  FH_MX_TILES(FH_X)
-#undef FH_X
-  return e;
-}
 
 // The tile shape with the least estimated time. Tiles are dealt out in rounds, one per CTA or CTA
 // pair; a round takes a fixed part and a part per stage, measured in back-to-back launches of

@@ -154,7 +154,6 @@ struct MxTile {
   bool pair;  // 256-row tiles on CTA pairs, each loading half of the tile's W rows
   int split;  // CTAs that share a tile, each a part of K (64-column tiles; else 1)
 };
-cudaError_t gemm_mx_prepare();
 MxTile gemm_mx_tile(int M, int N, int K, int fmt, int sms);
 inline bool gemm_mx_tma_out(int N, int out_kind) { return N % (out_kind == 0 ? 4 : out_kind == 1 ? 8 : 32) == 0; }
 int gemm_mx_out_row_bytes(MxTile t, int out_kind);  // of a staging box: 16, 32, 64 or 128
