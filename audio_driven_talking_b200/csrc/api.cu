@@ -1459,7 +1459,7 @@ int fh_op_linear_mx(const void* A, const void* A_scales, const void* W, const vo
   const uint64_t orow = (uint64_t)N * (out_type == FH_F32 ? 8 : out_type == FH_BF16 ? 4 : out_type == FH_MXFP8 ? 2 : 1) / 2;
   if (gemm_mx_tma_out(N, out_type) && !make_mx_out_map(&maps.o, out, M, orow, gemm_mx_out_row_bytes(t, out_type)))
     return fail(FH_ERR_CUDA, "tensor map encoding");
-  if (!make_mx_maps(&maps.a, &maps.sa, A, A_scales, M, pitch, K, 128, kt, 1) ||
+  if (!make_mx_maps(&maps.a, &maps.sa, A, A_scales, M, pitch, K, gemm_mx_a_rows(t, M), kt, 1) ||
       !make_mx_maps(&maps.w, &maps.sw, W, W_scales, N, pitch, K, t.pair ? t.bn / 2 : t.bn, kt, (t.bn + 127) / 128))
     return fail(FH_ERR_CUDA, "tensor map encoding");
   cudaError_t e = gemm_mx(maps, t, bias, out, out_scales, M, N, K, mx_fmt(mxtype), act == FH_ACT_GELU, out_type, sms,

@@ -202,6 +202,7 @@ struct MxParams {
   int M, N, nk;      // nk: stages along K
   int last;          // MMAs of the last stage
   int split;         // CTAs that share a tile
+  uint32_t tx;       // bytes that fill a stage
   int num_m, ntiles;
   int wide;  // 256-column tiles: those from here on are taken as two halves each
   int gelu;
@@ -288,6 +289,7 @@ __device__ __forceinline__ void copy_box(const MxParams& p, uint8_t* box, int ro
   using T = typename std::conditional<OUT == MXO_F32, float, bf16>::type;
   constexpr int PER = 16 / (int)sizeof(T);
   const int rows = min(32, p.M - row0);
+#pragma unroll 8
   for (int r = 0; r < rows; ++r) {
     T* dst = reinterpret_cast<T*>(p.out) + (long)(row0 + r) * p.N + col;
 #pragma unroll
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
         if (elect_one()) {
           uint8_t* sa = smem + cur.i * S::OPER_BYTES;
           uint8_t* sf = smem + S::SF_OFF + cur.i * S::SF_BYTES;
-          if (rank == 0) mbar_expect_tx(&full[cur.i], S::TX_BYTES);
+          if (rank == 0) mbar_expect_tx(&full[cur.i], p.tx);
           load_codes<PAIR>(&tmA, &full[cur.i], sa, kb * 32, m0);
           load_codes<PAIR>(&tmW, &full[cur.i], sa + S::A_BYTES, kb * 32, w0);
           load_scales<PAIR>(&tmSA, &full[cur.i], sf, kb * S::ATOMS, m0 >> 7);
@@ -755,6 +757,7 @@ cudaError_t launch_mx(const MxMaps& maps, MxParams p, int K, int sms, cudaStream
   p.nk = (K + S::KB - 1) / S::KB;
   p.last = (K - (p.nk - 1) * S::KB + S::KB / 4 - 1) / (S::KB / 4);
   p.num_m = (p.M + S::TM - 1) / S::TM;
+  p.tx = S::TX_BYTES - (128 - gemm_mx_a_rows({BN, PAIR, 1}, p.M)) * 128 * (PAIR ? 2 : 1);
   // a microscaled output's scale tiles are written whole: tiles up to the next multiple of 128
   const int ncols = OUT >= MXO_FP8 ? (p.N + 127) / 128 * 128 : p.N;
   const long tiles = (long)p.num_m * ((ncols + BN - 1) / BN);
@@ -834,7 +837,7 @@ MxTile gemm_mx_tile(int M, int N, int K, int fmt, int sms) {
   float least = 0.f;
   for (const auto& s : shapes) {
     const int tm = s.t.pair ? 256 : 128, slots = s.t.pair ? sms / 2 : sms;
-    if (slots < 1) continue;
+    if (slots < 1 || (s.t.pair && M <= 128)) continue;  // a pair's second CTA would have no rows
     const long tiles = (long)((M + tm - 1) / tm) * ((N + s.t.bn - 1) / s.t.bn);
     float us = (float)((tiles + slots - 1) / slots) * (nk * s.stage[fmt] + s.fixed);
     if (s.t.bn == 256 && wide_tiles(tiles, slots) < tiles)  // the last round is one of 128 columns
@@ -854,6 +857,11 @@ MxTile gemm_mx_tile(int M, int N, int K, int fmt, int sms) {
   }
   return best;
 }
+
+// Rows of A that a load brings: not the 127 past a single one, which take as long to fill with zeros
+// as they would to read (1 x 9216 x 1536 mxfp8: 9.0 us with them). What lies in the other rows of
+// shared memory makes results of rows that no one stores.
+int gemm_mx_a_rows(MxTile t, int M) { return t.pair || M >= 128 ? 128 : (M + 7) / 8 * 8; }
 
 int gemm_mx_out_row_bytes(MxTile t, int out_kind) { return box_row_bytes(out_kind, t.bn / 2); }
 

@@ -142,7 +142,7 @@ cudaError_t mx_dequantize(const void* data, const void* scales, int M, int K, in
 cudaError_t add_rms_norm(const void* x, bool x_bf16, const void* res, bool res_bf16, void* sum, const float* a,
                          const float* c, long bstride, int rows_per_batch, int M, int D, float eps, int out_kind,
                          void* out, void* scales, cudaStream_t st);
-// The product's TMA maps: codes as bytes (box 128 x rows, 128-byte swizzle), scale tiles as
+// The product's TMA maps: codes as bytes (box 128 x rows, 128-byte swizzle; `a`: gemm_mx_a_rows), scale tiles as
 // [row tiles][K tiles][128 words] (box 128 words x tiles per stage x row tiles).
 // `o`: the output as 32-bit words, box (row bytes / 4) x 32, swizzle of the row bytes; not used
 // where gemm_mx_tma_out() says that rows of N results are not 16-byte aligned.
@@ -156,6 +156,7 @@ struct MxTile {
 };
 MxTile gemm_mx_tile(int M, int N, int K, int fmt, int sms);
 inline bool gemm_mx_tma_out(int N, int out_kind) { return N % (out_kind == 0 ? 4 : out_kind == 1 ? 8 : 32) == 0; }
+int gemm_mx_a_rows(MxTile t, int M);                // rows of the box of A's map
 int gemm_mx_out_row_bytes(MxTile t, int out_kind);  // of a staging box: 16, 32, 64 or 128
 cudaError_t gemm_mx(const MxMaps& maps, MxTile t, const float* bias, void* out, void* oscales, int M, int N, int K,
                     int fmt, bool gelu, int out_kind, int sms, cudaStream_t st);
