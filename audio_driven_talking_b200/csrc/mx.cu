@@ -50,6 +50,7 @@ __device__ __forceinline__ void unpack16(const uint32_t (&w)[4 * sizeof(T)], flo
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
   }
 }
+
 template <typename T, MxFormat F, int QU>
 __global__ void __launch_bounds__(QT_THREADS) quantize_kernel(const T* __restrict__ x, long ldx, int M, int K,
                                                               unsigned ktiles, unsigned units,
@@ -213,6 +214,7 @@ struct Raw8 {
       v[i] = __uint_as_float(sizeof(T) == 4 ? w[i] : i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
 };
+
 template <typename TX, typename TR, int OUT, int W, int NC>
 __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
     add_rms_norm_kernel(const TX* x, const TR* res, TX* sum, const float* __restrict__ a,
@@ -317,11 +319,14 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
   }
 }
 
-// Warps to a row and chunks to a lane, the first pair that the row fits. Measured: two or three
-// chunks a lane keep enough bytes in flight without starving the SM of warps (23040 x 1536 of fp32
-// and bf16: 66 us with 4 warps of 2, 75 with 1 of 6, 72 with 8 of 1); rows of bf16, half as many
-// bytes, want more chunks a lane (40 us with 2 of 3, 45 with 4 of 2); and of up to 256 rows each
-// is a latency (128 x 1536: 2.6 us with 8 of 1, 3.0 with 4 of 2).
+// Warps to a row and chunks to a lane, the first pair that the row fits. Measured at 128 to 160 MB: rows
+// of fp32 are fastest at two chunks a lane, which keep enough bytes in flight without starving the SM of
+// warps (1536 columns, fp32 and bf16: 36.0 us with 3 warps of 2, 37.8 with 2 of 3, 38.8 with 6 of 1; only 11
+// or 12 warps of two leave the SM half empty: 6144 columns 43.4, 8 of 3 40.9); rows of bf16, half as many
+// bytes, at three or four, whichever leaves fewer lanes idle (1536 columns: 26.2 us with 2 of 3, 28.1 with
+// 3 of 2; 4000 columns: 28.5 with 4 of 4, 30.4 with 6 of 3). Up to 256 rows each is a latency (100 x 1536:
+// 2.6 us with 8 of 1, 3.0 with 4 of 2). The pairs are compiled: with the count of warps known at run time only,
+// a row's addresses cost up to a tenth (30000 x 1568 bf16 66 us, 59 compiled).
 template <typename TX, typename TR, int OUT>
 cudaError_t launch_norm(const void* x, const void* res, void* sum, const float* a, const float* c, long bstride,
                         int rows_per_batch, int M, int D, float eps, void* out, uint8_t* scales, cudaStream_t st) {
@@ -334,17 +339,35 @@ cudaError_t launch_norm(const void* x, const void* res, void* sum, const float* 
                     dim3(WV == 1 ? 128 : 32 * WV), 0, st, (const TX*)x, (const TR*)res, (TX*)sum, a, c, bstride,      \
                     rows_per_batch, M, rows, D, eps, wide, out, scales)
   FH_NORM(1, 1);
+  if (M <= 256) {
+    FH_NORM(2, 1);
+    FH_NORM(4, 1);
+    FH_NORM(8, 1);
+    FH_NORM(16, 1);
+  }
   FH_NORM(1, 2);
-  if (M <= 256) FH_NORM(8, 1);
-  FH_NORM(2, 2);
-  if constexpr (sizeof(TX) == 2) FH_NORM(2, 3);
-  FH_NORM(4, 2);
-  if constexpr (sizeof(TX) == 2) FH_NORM(4, 4);
-  FH_NORM(8, 2);
-  FH_NORM(8, 3);
-  FH_NORM(8, 4);
-  FH_NORM(8, 6);
-  FH_NORM(8, 8);
+  if constexpr (sizeof(TX) == 2) {
+    FH_NORM(1, 4);
+    FH_NORM(2, 3);
+    FH_NORM(2, 4);
+    FH_NORM(3, 3);
+    FH_NORM(4, 3);
+    FH_NORM(4, 4);
+    FH_NORM(5, 4);
+    FH_NORM(8, 3);
+    FH_NORM(8, 4);
+  } else {
+    FH_NORM(2, 2);
+    FH_NORM(3, 2);
+    FH_NORM(4, 2);
+    FH_NORM(5, 2);
+    FH_NORM(6, 2);
+    FH_NORM(8, 2);
+    FH_NORM(10, 2);
+    FH_NORM(8, 3);
+    FH_NORM(16, 2);
+  }
+  FH_NORM(16, 4);
 #undef FH_NORM
   return cudaErrorInvalidValue;
 }

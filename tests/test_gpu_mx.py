@@ -171,6 +171,18 @@ def test_add_rms_norm(M, D, streams, mod, xt, rt, out):
         assert torch.equal(y, again)
 
 
+@pytest.mark.parametrize("M", [3, 256, 259])
+@pytest.mark.parametrize("D", [64, 256, 480, 512, 640, 1024, 1280, 1792, 2048, 2240, 2400, 2720, 3616, 4096, 4640, 5344, 6144, 8192, 12320])
+def test_add_rms_norm_widths(D, M):
+    """Row widths at and between the shapes that share a row, for few rows and many."""
+    for xt, rt, mod, out in ((F32, BF, True, "mxfp8"), (BF, BF, False, "mxfp4"), (BF, F32, True, BF), (F32, F32, False, F32)):
+        x, res = dev(4 * randn(M + D, M, D), xt), dev(randn(M + D + 1, M, D), rt)
+        a, c = dev(1 + 0.1 * randn(D, D)), dev(0.3 * randn(D + 1, D)) if mod else None
+        total, y = fh.add_rms_norm(x, res, a, c, out=out)
+        assert torch.equal(total, (x.float() + res.float()).to(xt))
+        check_any(y, *norm_reference(f64(total), f64(a), None if c is None else f64(c), 1, 1e-6))
+
+
 def test_add_rms_norm_in_place_and_zero_rows():
     x, res = dev(randn(1, 50, 1536)), dev(randn(2, 50, 1536))
     x[7] = 0
