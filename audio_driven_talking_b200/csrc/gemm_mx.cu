@@ -20,7 +20,8 @@
 // against 59.3). What bounds the loop now is shared memory: a stage's 32 KB are written by TMA and
 // read by the MMAs at 128 bytes a clock each SM, 512 of the about 600 clocks that a stage of a
 // 256 x 256 tile takes.
-// Every wait is bounded (FH_WAIT_LIMIT_NS), as in gemm_tc.cu.
+// Every wait is bounded (FH_WAIT_LIMIT_NS), as in gemm_tc.cu; an operator call has no error word to
+// report one that ran out in.
 #include <atomic>
 #include <type_traits>
 
@@ -380,8 +381,8 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 // mbar_wait (common.cuh: bounded, false on giving up) by a whole warp, with one answer
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err) {
-  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || mbar_wait(bar, parity, abort, err, ERRBIT_TIMEOUT_GEMM));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || mbar_wait(bar, parity, abort, nullptr, 0u));
 }
 
 // Whether the phase is complete, without waiting
@@ -440,7 +441,7 @@ template <MxFormat F, int BN, bool PAIR, int OUT, bool SPLIT>
 __global__ void __launch_bounds__(MXG_THREADS, 1)
     gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSW,
-                   const __grid_constant__ CUtensorMap tmO, MxParams p, unsigned* err) {
+                   const __grid_constant__ CUtensorMap tmO, MxParams p) {
   using S = MxShape<F, BN, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
       // a narrow tile's box has W rows beyond it, which no MMA reads
       const int w0 = at.n0 + (int)rank * (at.narrow ? S::WROWS / 2 : S::WROWS);
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!warp_wait(&empty[cur.i], cur.phase ^ 1u, abort_flag, err)) {
+        if (!warp_wait(&empty[cur.i], cur.phase ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
         st += S::STAGES;
         ph ^= 1u;
       }
-      ok = warp_wait(&empty[st], ph, abort_flag, err);
+      ok = warp_wait(&empty[st], ph, abort_flag);
     }
     if (!ok) {  // give copies already issued time to land
       const uint64_t t0 = globaltimer();
@@ -561,9 +562,9 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
         // of the preceding tile's accumulator that this one overlaps has been read, by threads
         // that had finished tile local - 2 before.
         if (BN == 256) {
-          if (local >= 1 && !warp_wait(&tempty[acc ^ 1], ((local - 1) >> 1) & 1, abort_flag, err)) break;
+          if (local >= 1 && !warp_wait(&tempty[acc ^ 1], ((local - 1) >> 1) & 1, abort_flag)) break;
         } else {
-          if (local >= 2 && !warp_wait(&tempty[acc], ((local - 2) >> 1) & 1, abort_flag, err)) break;
+          if (local >= 2 && !warp_wait(&tempty[acc], ((local - 2) >> 1) & 1, abort_flag)) break;
         }
         const uint32_t d_tmem = tmem_base + acc * S::ACC1;
         // the tile's first W row within its scale row tile (BN = 64, 192): 32 rows a column
@@ -573,13 +574,13 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
         for (int kb = kb0; kb < kb1; ++kb) {
           if constexpr (S::NSF < S::STAGES) {
             if (pending == S::NSF) {
-              ok = warp_wait(&empty[done.i], done.phase, abort_flag, err);
+              ok = warp_wait(&empty[done.i], done.phase, abort_flag);
               done.next();
             } else {
               ++pending;
             }
           }
-          ok = ok && (__all_sync(0xffffffffu, ready) || warp_wait(&full[cur.i], cur.phase, abort_flag, err));
+          ok = ok && (__all_sync(0xffffffffu, ready) || warp_wait(&full[cur.i], cur.phase, abort_flag));
           if (!ok) break;
           const int sfi = S::NSF < S::STAGES ? sf_next : cur.i, stage = cur.i;
           cur.next();
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
       // tail: the epilogues have released the last accumulators (no arrival left in flight)
       for (int i = 0; i < 2 && i < local; ++i) {
         const int t = local - 1 - i;
-        if (!warp_wait(&tempty[t & 1], (t >> 1) & 1, abort_flag, err)) break;
+        if (!warp_wait(&tempty[t & 1], (t >> 1) & 1, abort_flag)) break;
       }
     }
   } else {
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
       if (lane < share / 4) bias[lane] = load_bias(p, n0 + 4 * lane);  // while the MMAs run
       __syncwarp();
       const int row0 = m0 + quarter * 32, row = row0 + lane;
-      if (!warp_wait(&tfull[acc], (local >> 1) & 1, abort_flag, err)) break;  // tcgen05.ld is warp-collective
+      if (!warp_wait(&tfull[acc], (local >> 1) & 1, abort_flag)) break;  // tcgen05.ld is warp-collective
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * S::ACC1 + sub * share;
       auto release = [&]() {
@@ -793,8 +794,7 @@ cudaError_t launch_mx(const MxMaps& maps, MxParams p, int K, int sms, cudaStream
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemm_mx_kernel<F, BN, PAIR, OUT, SPLIT>, maps.a, maps.w, maps.sa, maps.sw, maps.o, p,
-                            (unsigned*)nullptr);
+  return cudaLaunchKernelEx(&cfg, gemm_mx_kernel<F, BN, PAIR, OUT, SPLIT>, maps.a, maps.w, maps.sa, maps.sw, maps.o, p);
 }
 
 template <MxFormat F, int BN, bool PAIR, bool SPLIT>

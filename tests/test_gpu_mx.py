@@ -319,9 +319,11 @@ def test_linear_mx_narrow_results(N, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("M,N,K", [(4096, 4096, 1536), (4097, 4224, 2080), (2500, 8961, 1536), (3900, 8960, 1568), (8640, 1536, 4096)])
+@pytest.mark.parametrize("M,N,K", [(4096, 4096, 1536), (4097, 4224, 2080), (2500, 8961, 1536), (3900, 8960, 1568), (8640, 1536, 4096),
+                                   (1280, 4608, 1536), (1300, 4641, 1568), (100, 12320, 544), (1, 16384, 1536), (64, 18000, 96)])
 def test_linear_mx_wide_tiles(M, N, K, fmt):
-    """Several rounds of 256-column tiles, the last one of halves, on ragged edges."""
+    """Several rounds of 256-column tiles, the last one of halves, on ragged edges; tiles of 192 columns;
+    and few rows against many columns."""
     A, W, bias = operands(M + N + K, M, N, K, fmt)
     y, tol = linear_reference(A, W, bias, "gelu")
     for out in (BF, F32, "mxfp8", "mxfp4") if N % 32 == 0 else (BF, F32):
