@@ -25,7 +25,8 @@ __device__ __forceinline__ void store8w(float* p, const float (&v)[8], bool wide
 // A warp takes units of 4 rows x 128 columns, 16 columns a lane: two lanes make a block, so its
 // maximum crosses lanes once, and the four scale bytes of a row are one word. QU units are loaded
 // before the first is worked on, and no warp waits for another. Bytes bound it: the values read
-// once, the codes and scales written once.
+// once, the codes and scales written once (8640 x 8960 bf16 to mxfp8: 37.0 us, 6.3 TB/s; with 8 values
+// a lane, four shuffles for them and a scale tile gathered by the CTA 60.5).
 constexpr int QT_THREADS = 256;
 
 // Sixteen consecutive values as they lie in memory: 4 * sizeof(T) words
@@ -111,7 +112,9 @@ cudaError_t launch_quantize(const void* x, long ldx, int M, int K, uint8_t* data
 }
 
 // ------------------------------------------------------------------ dequantise
-// One CTA per scale tile, 128 rows x 128 columns; sixteen lanes take a row, 8 values each.
+// One CTA per scale tile, 128 rows x 128 columns; sixteen lanes take a row, 8 values each, eight rows in
+// flight. Bytes bound it: 8640 x 8960 mxfp8 to bf16 37.2 us (6.3 TB/s), to fp32 64 (86 with 16-byte stores,
+// which leave half of each sector to the next).
 template <typename T, MxFormat F>
 __global__ void __launch_bounds__(QT_THREADS) dequantize_kernel(const uint8_t* __restrict__ data,
                                                                 const uint8_t* __restrict__ scales, int M, int K,
@@ -170,6 +173,7 @@ __global__ void __launch_bounds__(QT_THREADS) dequantize_kernel(const uint8_t* _
 // are read once, the sum and y written once, so bytes bound it. A lane's loads are all in flight
 // together: they are predicated, not branched around, since a branch waits for its own. Four lanes
 // make a microscaled block. Rows past M up to the end of the last scale tile only get zero scales.
+// 23040 x 1536 fp32 + bf16 to mxfp8, 390 MB: 63 us, 6.2 TB/s.
 enum NormOut { NO_F32 = 0, NO_BF16 = 1, NO_FP8 = 2, NO_FP4 = 3 };
 
 // A row's 1 / rms as r + lo: the reciprocal root is good to 2 steps, and a Newton step on its
