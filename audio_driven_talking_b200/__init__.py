@@ -118,6 +118,8 @@ def load_library() -> ctypes.CDLL:
         "fh_op_quantize": (I, [P, ctypes.c_long, I, I, I, I, P, P, P]),
         "fh_op_dequantize": (I, [P, P, I, I, I, P, I, P]),
         "fh_op_add_rms_norm": (I, [P, I, P, I, P, P, P, ctypes.c_long, I, I, I, F, I, P, P, P]),
+        "fh_op_sync": (I, [P]),
+        "fh_op_probe_wait_timeout": (I, [P]),
         "fh_op_linear_mx": (I, [P, P, P, P, P, I, I, I, I, I, I, P, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -466,6 +468,12 @@ def linear_mx(A, W, bias=None, act=None, out=None, stream=None):
     return _on_stream(stream, A, (A, W, bias), lambda: bind.linear_mx(A, W, bias, act, out))
 
 
+def sync_operators(stream=None):
+    """Wait for `stream` (torch's current one) and raise FHError if a kernel-side wait of linear_mx ran
+    out on the current device since the last report; the next linear_mx would raise it too."""
+    _check(load_library().fh_op_sync(_stream(stream)))
+
+
 __all__ = ["DiT", "ModelConfig", "LITE", "FP32_BLOCK", "ONE_BLOCK", "LITE_768_X3", "FHError", "load_library",
            "linear", "attention", "cross_attention", "row_norm", "MXTensor", "quantize", "dequantize", "add_rms_norm",
-           "linear_mx", "FH_F32", "FH_BF16", "FH_MXFP8", "FH_MXFP4"]
+           "linear_mx", "sync_operators", "FH_F32", "FH_BF16", "FH_MXFP8", "FH_MXFP4"]

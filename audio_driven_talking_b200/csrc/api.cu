@@ -9,6 +9,7 @@
 // is the caller-owned workspace; Methods > talk runs slice by slice. The launch
 // sequence of one block is the Wan-style adaLN block of readings R1-R11.
 #include <algorithm>
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -653,6 +654,41 @@ int common_checks(fh_dit* m, int batch, void* ws) {
 // first calls from several threads do not race on it
 std::mutex g_prepare_mu;
 bool g_prepared[64] = {};
+// The operators' error word of a device, host memory that its kernels can write: a wait that ran out
+// is latched there. Allocated at the first call that needs it, also while a stream captures.
+struct OpError {
+  std::atomic<unsigned*> host{nullptr};
+  unsigned* dev = nullptr;
+};
+OpError g_op_error[64];
+
+int op_error_word(int dev, OpError** out) {
+  if (dev < 0 || dev >= 64) return fail(FH_ERR_UNSUPPORTED, "device ordinal %d outside [0, 64)", dev);
+  OpError& w = g_op_error[dev];
+  *out = &w;
+  if (w.host.load(std::memory_order_acquire)) return FH_OK;
+  std::lock_guard<std::mutex> lock(g_prepare_mu);
+  if (w.host.load(std::memory_order_relaxed)) return FH_OK;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  CK(cudaThreadExchangeStreamCaptureMode(&mode));
+  unsigned* host = nullptr;
+  cudaError_t e = cudaHostAlloc((void**)&host, sizeof(unsigned), cudaHostAllocMapped);
+  if (e == cudaSuccess) e = cudaHostGetDevicePointer((void**)&w.dev, host, 0);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return fail(FH_ERR_CUDA, "operators' error word: %s", cudaGetErrorString(e));
+  *host = 0;
+  w.host.store(host, std::memory_order_release);
+  return FH_OK;
+}
+
+// Reports and clears what the word holds
+int take_op_error(OpError& w) {
+  unsigned* host = w.host.load(std::memory_order_acquire);
+  if (!host || !*reinterpret_cast<volatile unsigned*>(host)) return FH_OK;
+  *reinterpret_cast<volatile unsigned*>(host) = 0;
+  return fail(FH_ERR_TIMEOUT, "a kernel-side wait of an earlier operator call on this device ran out; its result is not valid");
+}
+
 int prepare_device(int dev) {
   if (dev < 0 || dev >= 64) return fail(FH_ERR_UNSUPPORTED, "device ordinal %d outside [0, 64)", dev);
   std::lock_guard<std::mutex> lock(g_prepare_mu);
@@ -1450,6 +1486,9 @@ int fh_op_linear_mx(const void* A, const void* A_scales, const void* W, const vo
   if (!load_encode()) return fail(FH_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled unavailable");
   int dev = 0, sms = 148;
   CK(cudaGetDevice(&dev));
+  OpError* word;
+  RUN(op_error_word(dev, &word));
+  RUN(take_op_error(*word));
   CK(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   const MxTile t = gemm_mx_tile(M, N, K, mx_fmt(mxtype), sms);
   const uint64_t pitch = mxtype == FH_MXFP4 ? K / 2 : K;
@@ -1463,8 +1502,25 @@ int fh_op_linear_mx(const void* A, const void* A_scales, const void* W, const vo
       !make_mx_maps(&maps.w, &maps.sw, W, W_scales, N, pitch, K, t.pair ? t.bn / 2 : t.bn, kt, (t.bn + 127) / 128))
     return fail(FH_ERR_CUDA, "tensor map encoding");
   cudaError_t e = gemm_mx(maps, t, bias, out, out_scales, M, N, K, mx_fmt(mxtype), act == FH_ACT_GELU, out_type, sms,
-                          reinterpret_cast<cudaStream_t>(stream));
+                          word->dev, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(FH_ERR_CUDA, "microscaled linear launch: %s", cudaGetErrorString(e));
+  return FH_OK;
+}
+
+int fh_op_sync(void* stream) {
+  int dev = 0;
+  CK(cudaGetDevice(&dev));
+  CK(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)));
+  if (dev < 0 || dev >= 64) return FH_OK;
+  return take_op_error(g_op_error[dev]);
+}
+
+int fh_op_probe_wait_timeout(void* stream) {
+  int dev = 0;
+  CK(cudaGetDevice(&dev));
+  OpError* word;
+  RUN(op_error_word(dev, &word));
+  CK(wait_probe(word->dev, reinterpret_cast<cudaStream_t>(stream)));
   return FH_OK;
 }
 

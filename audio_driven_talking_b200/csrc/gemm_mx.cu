@@ -22,8 +22,8 @@
 // 256 x 256 tile takes: 4096^3 mxfp8 48.7 us (2820 TFLOP/s), 4096 x 4096 x 8192 mxfp4 48 (5700); for a
 // second and longer the power cap holds the clock below that. With few stages a tile and GELU the epilogue
 // bounds it: 8640 x 8960 x 1536 mxfp4 67 us.
-// Every wait is bounded (FH_WAIT_LIMIT_NS), as in gemm_tc.cu; an operator call has no error word to
-// report one that ran out in.
+// Every wait is bounded (FH_WAIT_LIMIT_NS), as in gemm_tc.cu; one that ran out is latched in the
+// device's error word of the operators.
 #include <atomic>
 #include <type_traits>
 
@@ -209,7 +209,8 @@ struct MxParams {
   int num_m, ntiles;
   int wide;  // 256-column tiles: those from here on are taken as two halves each
   int gelu;
-  int tma;  // rows of out are 16-byte aligned: boxes leave by TMA
+  int tma;        // rows of out are 16-byte aligned: boxes leave by TMA
+  unsigned* err;  // where a wait that ran out is latched
 };
 
 // One row's 32 consecutive results: bias (of these columns, in shared memory), activation.
@@ -383,8 +384,8 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 // mbar_wait (common.cuh: bounded, false on giving up) by a whole warp, with one answer
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || mbar_wait(bar, parity, abort, nullptr, 0u));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || mbar_wait(bar, parity, abort, err, ERRBIT_TIMEOUT_GEMM));
 }
 
 // Whether the phase is complete, without waiting
@@ -513,7 +514,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
       // a narrow tile's box has W rows beyond it, which no MMA reads
       const int w0 = at.n0 + (int)rank * (at.narrow ? S::WROWS / 2 : S::WROWS);
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!warp_wait(&empty[cur.i], cur.phase ^ 1u, abort_flag)) {
+        if (!warp_wait(&empty[cur.i], cur.phase ^ 1u, abort_flag, p.err)) {
           ok = false;
           break;
         }
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
         st += S::STAGES;
         ph ^= 1u;
       }
-      ok = warp_wait(&empty[st], ph, abort_flag);
+      ok = warp_wait(&empty[st], ph, abort_flag, p.err);
     }
     if (!ok) {  // give copies already issued time to land
       const uint64_t t0 = globaltimer();
@@ -564,9 +565,9 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
         // of the preceding tile's accumulator that this one overlaps has been read, by threads
         // that had finished tile local - 2 before.
         if (BN == 256) {
-          if (local >= 1 && !warp_wait(&tempty[acc ^ 1], ((local - 1) >> 1) & 1, abort_flag)) break;
+          if (local >= 1 && !warp_wait(&tempty[acc ^ 1], ((local - 1) >> 1) & 1, abort_flag, p.err)) break;
         } else {
-          if (local >= 2 && !warp_wait(&tempty[acc], ((local - 2) >> 1) & 1, abort_flag)) break;
+          if (local >= 2 && !warp_wait(&tempty[acc], ((local - 2) >> 1) & 1, abort_flag, p.err)) break;
         }
         const uint32_t d_tmem = tmem_base + acc * S::ACC1;
         // the tile's first W row within its scale row tile (BN = 64, 192): 32 rows a column
@@ -576,13 +577,13 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
         for (int kb = kb0; kb < kb1; ++kb) {
           if constexpr (S::NSF < S::STAGES) {
             if (pending == S::NSF) {
-              ok = warp_wait(&empty[done.i], done.phase, abort_flag);
+              ok = warp_wait(&empty[done.i], done.phase, abort_flag, p.err);
               done.next();
             } else {
               ++pending;
             }
           }
-          ok = ok && (__all_sync(0xffffffffu, ready) || warp_wait(&full[cur.i], cur.phase, abort_flag));
+          ok = ok && (__all_sync(0xffffffffu, ready) || warp_wait(&full[cur.i], cur.phase, abort_flag, p.err));
           if (!ok) break;
           const int sfi = S::NSF < S::STAGES ? sf_next : cur.i, stage = cur.i;
           cur.next();
@@ -611,7 +612,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
       // tail: the epilogues have released the last accumulators (no arrival left in flight)
       for (int i = 0; i < 2 && i < local; ++i) {
         const int t = local - 1 - i;
-        if (!warp_wait(&tempty[t & 1], (t >> 1) & 1, abort_flag)) break;
+        if (!warp_wait(&tempty[t & 1], (t >> 1) & 1, abort_flag, p.err)) break;
       }
     }
   } else {
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1)
       if (lane < share / 4) bias[lane] = load_bias(p, n0 + 4 * lane);  // while the MMAs run
       __syncwarp();
       const int row0 = m0 + quarter * 32, row = row0 + lane;
-      if (!warp_wait(&tfull[acc], (local >> 1) & 1, abort_flag)) break;  // tcgen05.ld is warp-collective
+      if (!warp_wait(&tfull[acc], (local >> 1) & 1, abort_flag, p.err)) break;  // tcgen05.ld is warp-collective
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * S::ACC1 + sub * share;
       auto release = [&]() {
@@ -868,8 +869,9 @@ int gemm_mx_a_rows(MxTile t, int M) { return t.pair || M >= 128 ? 128 : (M + 7) 
 int gemm_mx_out_row_bytes(MxTile t, int out_kind) { return box_row_bytes(out_kind, t.bn / 2); }
 
 cudaError_t gemm_mx(const MxMaps& maps, MxTile t, const float* bias, void* out, void* oscales, int M, int N, int K,
-                    int fmt, bool gelu, int out_kind, int sms, cudaStream_t st) {
+                    int fmt, bool gelu, int out_kind, int sms, unsigned* err, cudaStream_t st) {
   MxParams p = {};
+  p.err = err;
   p.bias = bias;
   p.out = out;
   p.oscales = (uint8_t*)oscales;

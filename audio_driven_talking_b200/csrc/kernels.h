@@ -159,6 +159,6 @@ inline bool gemm_mx_tma_out(int N, int out_kind) { return N % (out_kind == 0 ? 4
 int gemm_mx_a_rows(MxTile t, int M);                // rows of the box of A's map
 int gemm_mx_out_row_bytes(MxTile t, int out_kind);  // of a staging box: 16, 32, 64 or 128
 cudaError_t gemm_mx(const MxMaps& maps, MxTile t, const float* bias, void* out, void* oscales, int M, int N, int K,
-                    int fmt, bool gelu, int out_kind, int sms, cudaStream_t st);
+                    int fmt, bool gelu, int out_kind, int sms, unsigned* err, cudaStream_t st);
 
 }  // namespace fh

@@ -108,10 +108,19 @@ enum fh_act { FH_ACT_NONE = 0, FH_ACT_GELU = 1 };
  * the block-scaled tensor core, accumulated in fp32; bias float32 or null; act FH_ACT_GELU: the
  * tanh form of GELU (results for arguments below -5.6 are off by up to 3e-9). K % 32 == 0; N any, but a multiple of 32 for a microscaled out. out_type any
  * of fh_dtype; out_scales for the microscaled ones, else null. A row or column with a NaN scale
- * gives NaN results. out may not overlap the operands. */
+ * gives NaN results. out may not overlap the operands. FH_ERR_TIMEOUT: a kernel-side wait of an earlier
+ * call on this device ran out; reported once, nothing is launched. */
 int fh_op_linear_mx(const void* A, const void* A_scales, const void* W, const void* W_scales, const float* bias,
                     int M, int N, int K, int mxtype, int act, int out_type, void* out, void* out_scales,
                     void* stream);
+
+/* Wait for `stream`, then report (FH_ERR_TIMEOUT) and clear what the microscaled product latched on the
+ * current device: a bounded kernel-side wait that ran out, so that a result since the last report is not
+ * valid. The next fh_op_linear_mx reports it too. */
+int fh_op_sync(void* stream);
+
+/* Make one such wait run out, as fh_dit_probe_wait_timeout below does for a model. */
+int fh_op_probe_wait_timeout(void* stream);
 
 /* Failure-detection check (no counterpart on the pages; reading of the pages'
  * reject-don't-hang stance): launches one CTA whose mbarrier wait has no arriving

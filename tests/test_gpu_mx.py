@@ -532,6 +532,22 @@ def test_other_streams():
     assert torch.equal(back, fh.dequantize(fh.quantize(x, "mxfp4")))
 
 
+def test_a_wait_that_ran_out_is_reported():
+    """A bounded wait of a kernel with no arriving party runs out (about a second): the next product
+    raises it once and launches nothing, as does sync_operators; the calls after them work."""
+    A, W, bias = operands(1, 40, 64, 64, "mxfp8")
+    want = fh.linear_mx(A, W, bias)
+    fh.sync_operators()
+    for report in (lambda: fh.linear_mx(A, W, bias), fh.sync_operators):
+        fh._check(fh.load_library().fh_op_probe_wait_timeout(torch.cuda.current_stream().cuda_stream))
+        torch.cuda.synchronize()
+        with pytest.raises(fh.FHError, match="ran out") as e:
+            report()
+        assert e.value.code == fh.FH_ERR_TIMEOUT
+        assert torch.equal(fh.linear_mx(A, W, bias), want)
+        fh.sync_operators()
+
+
 def test_calls_from_several_threads():
     """Threads with streams of their own, at once: checks, allocations and launches share nothing."""
     import threading
