@@ -98,7 +98,8 @@ bool out_kind(PyObject* o, int* kind) {
   return value_error("out=%R: expected torch.float32, torch.bfloat16, 'mxfp8' or 'mxfp4'", o);
 }
 
-// A CUDA tensor, on `device` where that is not negative; null with an error set
+// A CUDA tensor, on `device` where that is not negative; null with an error set. Those that torch.vmap
+// and the transforms of torch.func pass on wrap another tensor and have no memory of their own.
 const at::Tensor* cuda_tensor(PyObject* o, const char* what, int device = -1) {
   if (!THPVariable_Check(o)) {
     type_error("%s: expected a torch tensor", what);
@@ -111,6 +112,10 @@ const at::Tensor* cuda_tensor(PyObject* o, const char* what, int device = -1) {
   }
   if (device >= 0 && t.get_device() != device) {
     value_error("%s is on cuda:%d, expected cuda:%d", what, (int)t.get_device(), device);
+    return nullptr;
+  }
+  if (!t.has_storage()) {
+    value_error("%s has no storage: the operators take plain tensors, not ones that a transform wraps", what);
     return nullptr;
   }
   return &t;
@@ -203,6 +208,9 @@ bool arg_count(Py_ssize_t n, Py_ssize_t want, const char* name) {
   return n == want || type_error("%s: expected %d arguments", name, (int)want);
 }
 
+// Pointers and the stream are read with the GIL held: reading them may throw, which must not happen
+// between Py_BEGIN_ALLOW_THREADS and Py_END_ALLOW_THREADS.
+const float* floats(const at::Tensor* t) { return t ? static_cast<const float*>(t->const_data_ptr()) : nullptr; }
 void* stream_of(int device) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream(); }
 
 // quantize(x, fmt)
@@ -221,10 +229,12 @@ PyObject* py_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int dev = x->get_device();
   c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
   Out q(M, K, code, dev);
+  const void* const xp = x->const_data_ptr();
+  const long ldx = M > 1 ? x->stride(0) : K;
+  void *const qp = q.data.data_ptr(), *const sp = q.scales.data_ptr(), *const st = stream_of(dev);
   int rc;
   Py_BEGIN_ALLOW_THREADS;
-  rc = fh_op_quantize(x->const_data_ptr(), M > 1 ? x->stride(0) : K, (int)M, (int)K, kind, code, q.data.data_ptr(),
-                      q.scales.data_ptr(), stream_of(dev));
+  rc = fh_op_quantize(xp, ldx, (int)M, (int)K, kind, code, qp, sp, st);
   Py_END_ALLOW_THREADS;
   return library_ok(rc) ? q.object() : nullptr;
   END_HANDLE_TH_ERRORS
@@ -238,10 +248,11 @@ PyObject* py_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!arg_count(n, 2, "dequantize") || !mx_operand(a[0], "q", -1, &q) || !dtype_kind(a[1], "dtype", &kind)) return nullptr;
   c10::cuda::CUDAGuard guard((c10::DeviceIndex)q.device);
   Out out(q.rows, q.cols, kind, q.device);
+  const void *const qp = q.data->const_data_ptr(), *const sp = q.scales->const_data_ptr();
+  void *const op = out.data.data_ptr(), *const st = stream_of(q.device);
   int rc;
   Py_BEGIN_ALLOW_THREADS;
-  rc = fh_op_dequantize(q.data->const_data_ptr(), q.scales->const_data_ptr(), (int)q.rows, (int)q.cols, q.code,
-                        out.data.data_ptr(), kind, stream_of(q.device));
+  rc = fh_op_dequantize(qp, sp, (int)q.rows, (int)q.cols, q.code, op, kind, st);
   Py_END_ALLOW_THREADS;
   return library_ok(rc) ? out.object() : nullptr;
   END_HANDLE_TH_ERRORS
@@ -296,13 +307,14 @@ PyObject* py_add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
   const at::Tensor sum = own ? empty(M, D, x->scalar_type(), dev) : THPVariable_Unpack(a[6]);
   Out y(M, D, kind, dev);
+  void* const tp = sum.data_ptr();
+  const void *const xp = x->const_data_ptr(), *const rp = res->const_data_ptr();
+  const float *const ap = floats(g), *const cp = floats(c);
+  void *const yp = y.data.data_ptr(), *const sp = y.scale_ptr(), *const st = stream_of(dev);
   int rc;
   Py_BEGIN_ALLOW_THREADS;
-  rc = fh_op_add_rms_norm(x->const_data_ptr(), xk, res->const_data_ptr(), rk, sum.data_ptr(),
-                          static_cast<const float*>(g->const_data_ptr()),
-                          c ? static_cast<const float*>(c->const_data_ptr()) : nullptr, streams > 1 ? D : 0,
-                          M > 0 ? (int)(M / streams) : 1, (int)M, (int)D, (float)eps, kind, y.data.data_ptr(),
-                          y.scale_ptr(), stream_of(dev));
+  rc = fh_op_add_rms_norm(xp, xk, rp, rk, tp, ap, cp, streams > 1 ? D : 0, M > 0 ? (int)(M / streams) : 1, (int)M,
+                          (int)D, (float)eps, kind, yp, sp, st);
   Py_END_ALLOW_THREADS;
   if (!library_ok(rc)) return nullptr;
   Ref s(own ? THPVariable_Wrap(sum) : Py_NewRef(a[6])), o(y.object());
@@ -346,12 +358,14 @@ PyObject* py_linear_mx(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   c10::cuda::CUDAGuard guard((c10::DeviceIndex)A.device);
   Out y(M, N, kind, A.device);
+  const void *const dA = A.data->const_data_ptr(), *const sA = A.scales->const_data_ptr();
+  const void *const dW = W.data->const_data_ptr(), *const sW = W.scales->const_data_ptr();
+  const float* const bp = floats(bias);
+  void *const yp = y.data.data_ptr(), *const sp = y.scale_ptr(), *const st = stream_of(A.device);
   int rc;
   Py_BEGIN_ALLOW_THREADS;
-  rc = fh_op_linear_mx(A.data->const_data_ptr(), A.scales->const_data_ptr(), W.data->const_data_ptr(),
-                       W.scales->const_data_ptr(), bias ? static_cast<const float*>(bias->const_data_ptr()) : nullptr,
-                       (int)M, (int)N, (int)K, A.code, gelu ? FH_ACT_GELU : FH_ACT_NONE, kind, y.data.data_ptr(),
-                       y.scale_ptr(), stream_of(A.device));
+  rc = fh_op_linear_mx(dA, sA, dW, sW, bp, (int)M, (int)N, (int)K, A.code, gelu ? FH_ACT_GELU : FH_ACT_NONE, kind, yp,
+                       sp, st);
   Py_END_ALLOW_THREADS;
   return library_ok(rc) ? y.object() : nullptr;
   END_HANDLE_TH_ERRORS
