@@ -448,7 +448,7 @@ def add_rms_norm(x, res, a, c=None, out="mxfp8", eps=1e-6, sum_out=None, stream=
     [rows, columns] are float32 or bfloat16 each; a and c float32 vectors of a row's width, or
     [streams, columns] where each of `streams` equal runs of rows has its own. Columns are a
     multiple of 32, at most 16384. The sum goes to a new tensor, or to `sum_out`, which may be x
-    itself (or res, where the types agree)."""
+    itself (or res, where the types agree) and shares no memory with the inputs otherwise."""
     bind = _bind or _load_bind()
     if stream is None:
         return bind.add_rms_norm(x, res, a, c, out, eps, sum_out)

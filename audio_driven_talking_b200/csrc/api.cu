@@ -1466,6 +1466,9 @@ int fh_op_add_rms_norm(const void* x, int x_dtype, const void* res, int res_dtyp
   const size_t xb = (size_t)M * D * (x_dtype == FH_F32 ? 4 : 2), rb = (size_t)M * D * (res_dtype == FH_F32 ? 4 : 2);
   if ((sum != x && overlaps(sum, xb, x, xb)) || ((sum != res || res_dtype != x_dtype) && overlaps(sum, xb, res, rb)))
     return fail(FH_ERR_ARG, "the sum overlaps an input");
+  // the vectors: read for every row, while other rows' sums are written
+  const size_t vb = ((size_t)((M - 1) / rows_per_batch) * bstride + D) * sizeof(float);
+  if (overlaps(sum, xb, a, vb) || (c && overlaps(sum, xb, c, vb))) return fail(FH_ERR_ARG, "the sum overlaps a or c");
   cudaError_t e = add_rms_norm(x, x_dtype == FH_BF16, res, res_dtype == FH_BF16, sum, a, c, bstride, rows_per_batch, M,
                                D, eps, out_type, out, out_scales, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(FH_ERR_CUDA, "add-RMS-norm launch: %s", cudaGetErrorString(e));

@@ -97,7 +97,7 @@ int fh_op_dequantize(const void* data, const void* scales, int M, int K, int mxt
  * x_dtype, res [M][D] in res_dtype (FH_F32 or FH_BF16); D % 32 == 0, D <= 16384; a, c float32
  * vectors of D, row r's at a + (r / rows_per_batch) * bstride (bstride % 4 == 0). out_type any
  * of fh_dtype; out_scales for the microscaled ones, else null. sum may be x, or res where its
- * type is x's; it may not overlap them otherwise, nor out anything. */
+ * type is x's; it may not overlap them otherwise, nor a or c, nor out anything. */
 int fh_op_add_rms_norm(const void* x, int x_dtype, const void* res, int res_dtype, void* sum, const float* a,
                        const float* c, long bstride, int rows_per_batch, int M, int D, float eps, int out_type,
                        void* out, void* out_scales, void* stream);
