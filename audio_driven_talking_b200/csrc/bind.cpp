@@ -7,6 +7,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/InferenceMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -303,6 +304,10 @@ PyObject* py_add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       value_error("sum_out: expected x's shape and type");
       return nullptr;
     }
+    if (s->is_inference() && !c10::InferenceMode::is_enabled()) {
+      value_error("sum_out: an inference tensor is written in inference mode only");
+      return nullptr;
+    }
   }
   c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
   const at::Tensor sum = own ? empty(M, D, x->scalar_type(), dev) : THPVariable_Unpack(a[6]);
@@ -317,6 +322,7 @@ PyObject* py_add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           (int)D, (float)eps, kind, yp, sp, st);
   Py_END_ALLOW_THREADS;
   if (!library_ok(rc)) return nullptr;
+  if (!own) sum.unsafeGetTensorImpl()->bump_version();  // autograd sees that what it saved was written
   Ref s(own ? THPVariable_Wrap(sum) : Py_NewRef(a[6])), o(y.object());
   return s.p && o.p ? PyTuple_Pack(2, s.p, o.p) : nullptr;
   END_HANDLE_TH_ERRORS
