@@ -7,6 +7,8 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
+#include <c10/core/GradMode.h>
 #include <c10/core/InferenceMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -117,6 +119,13 @@ const at::Tensor* cuda_tensor(PyObject* o, const char* what, int device = -1) {
   }
   if (!t.has_storage()) {
     value_error("%s has no storage: the operators take plain tensors, not ones that a transform wraps", what);
+    return nullptr;
+  }
+  // forward only: what autograd would lose without a word is refused
+  if ((t.requires_grad() && c10::GradMode::is_enabled()) ||
+      (t._fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode())) {
+    value_error("%s requires a gradient, which these operators do not give: detach it, or call them in torch.no_grad()",
+                what);
     return nullptr;
   }
   return &t;
