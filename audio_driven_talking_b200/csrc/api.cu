@@ -48,17 +48,30 @@ int fail(int code, const char* fmt, ...) {
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+typedef CUresult (*CurrentFn)(CUcontext*);
 EncodeTiledFn g_encode = nullptr;
+CurrentFn g_current = nullptr;
+std::once_flag g_driver_once;
 
-bool load_encode() {
-  if (g_encode) return true;
-  void* fn = nullptr;
+bool driver_call(const char* name, void** fn) {
   cudaDriverEntryPointQueryResult q;
-  if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) != cudaSuccess ||
-      q != cudaDriverEntryPointSuccess || !fn)
-    return false;
-  g_encode = reinterpret_cast<EncodeTiledFn>(fn);
-  return true;
+  return cudaGetDriverEntryPoint(name, fn, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess && *fn;
+}
+
+// Before tensor maps are encoded, which needs a context bound to the calling thread. Launches and the
+// like bind the device's; in a thread whose first CUDA call this is, nothing has.
+bool load_encode() {
+  std::call_once(g_driver_once, [] {
+    void *encode = nullptr, *current = nullptr;
+    if (!driver_call("cuTensorMapEncodeTiled", &encode) || !driver_call("cuCtxGetCurrent", &current)) return;
+    g_encode = reinterpret_cast<EncodeTiledFn>(encode);
+    g_current = reinterpret_cast<CurrentFn>(current);
+  });
+  if (!g_encode) return false;
+  CUcontext bound = nullptr;
+  if (g_current(&bound) == CUDA_SUCCESS && bound) return true;
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
 }
 
 // 2D bf16 view [rows, cols] (cols contiguous), box 64 x box_rows, 128-byte swizzle.
