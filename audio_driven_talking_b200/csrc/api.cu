@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "epilogue.cuh"
+#include "error_word.h"
 #include "fh.h"
 #include "fh_ops.h"
 #include "kernels.h"
@@ -667,17 +668,13 @@ int common_checks(fh_dit* m, int batch, void* ws) {
 // first calls from several threads do not race on it
 std::mutex g_prepare_mu;
 bool g_prepared[64] = {};
-// The operators' error word of a device, host memory that its kernels can write: a wait that ran out
-// is latched there. Allocated at the first call that needs it, also while a stream captures.
-struct OpError {
-  std::atomic<unsigned*> host{nullptr};
-  unsigned* dev = nullptr;
-};
-OpError g_op_error[64];
+// The operators' error word of a device: a wait that ran out is latched there. Allocated at the first
+// call that needs it, also while a stream captures.
+ErrorWord g_op_error[64];
 
-int op_error_word(int dev, OpError** out) {
+int op_error_word(int dev, ErrorWord** out) {
   if (dev < 0 || dev >= 64) return fail(FH_ERR_UNSUPPORTED, "device ordinal %d outside [0, 64)", dev);
-  OpError& w = g_op_error[dev];
+  ErrorWord& w = g_op_error[dev];
   *out = &w;
   if (w.host.load(std::memory_order_acquire)) return FH_OK;
   std::lock_guard<std::mutex> lock(g_prepare_mu);
@@ -695,10 +692,8 @@ int op_error_word(int dev, OpError** out) {
 }
 
 // Reports and clears what the word holds
-int take_op_error(OpError& w) {
-  unsigned* host = w.host.load(std::memory_order_acquire);
-  if (!host || !*reinterpret_cast<volatile unsigned*>(host)) return FH_OK;
-  *reinterpret_cast<volatile unsigned*>(host) = 0;
+int take_op_error(ErrorWord& w) {
+  if (!w.take()) return FH_OK;
   return fail(FH_ERR_TIMEOUT, "a kernel-side wait of an earlier operator call on this device ran out; its result is not valid");
 }
 
@@ -1502,7 +1497,7 @@ int fh_op_linear_mx(const void* A, const void* A_scales, const void* W, const vo
   if (!load_encode()) return fail(FH_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled unavailable");
   int dev = 0, sms = 148;
   CK(cudaGetDevice(&dev));
-  OpError* word;
+  ErrorWord* word;
   RUN(op_error_word(dev, &word));
   RUN(take_op_error(*word));
   CK(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
@@ -1534,7 +1529,7 @@ int fh_op_sync(void* stream) {
 int fh_op_probe_wait_timeout(void* stream) {
   int dev = 0;
   CK(cudaGetDevice(&dev));
-  OpError* word;
+  ErrorWord* word;
   RUN(op_error_word(dev, &word));
   CK(wait_probe(word->dev, reinterpret_cast<cudaStream_t>(stream)));
   return FH_OK;
