@@ -683,7 +683,10 @@ int op_error_word(int dev, ErrorWord** out) {
   CK(cudaThreadExchangeStreamCaptureMode(&mode));
   unsigned* host = nullptr;
   cudaError_t e = cudaHostAlloc((void**)&host, sizeof(unsigned), cudaHostAllocMapped);
-  if (e == cudaSuccess) e = cudaHostGetDevicePointer((void**)&w.dev, host, 0);
+  if (e == cudaSuccess) {
+    e = cudaHostGetDevicePointer((void**)&w.dev, host, 0);
+    if (e != cudaSuccess) cudaFreeHost(host);
+  }
   cudaThreadExchangeStreamCaptureMode(&mode);
   if (e != cudaSuccess) return fail(FH_ERR_CUDA, "operators' error word: %s", cudaGetErrorString(e));
   *host = 0;

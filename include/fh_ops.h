@@ -2,7 +2,9 @@
  * fh_ops.h - operator-level entry points of the FlashHead DiT library, for unit
  * parity tests of single kernels. Same conventions as fh.h (return codes,
  * fh_last_error, caller-owned 16-byte-aligned device pointers, asynchronous on
- * `stream`). They allocate nothing.
+ * `stream`). They allocate no device memory, and nothing else but one word of mapped host memory per
+ * device, at the first fh_op_linear_mx or fh_op_probe_wait_timeout there (also while a stream captures),
+ * kept for the process: the error word that fh_op_sync reports.
  *
  * Microscaled tensors (types FH_MXFP8 and FH_MXFP4) of M rows x K columns, K % 32 == 0, hold a
  * number as an element times its block's scale; a block is 32 consecutive values of a row.
