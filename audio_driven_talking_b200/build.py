@@ -70,10 +70,19 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     return LIB
 
 
+def _bind_made_for() -> str:
+    """What the binding module was compiled against besides this project's files."""
+    import torch
+    return f"{torch.__version__} {torch.version.git_version} {sys.implementation.cache_tag} {os.path.dirname(torch.__file__)}"
+
+
 def _build_bind(force: bool) -> None:
-    """Compile the binding module, which takes its tensors from torch and links to libfh.so."""
+    """Compile the binding module, which takes its tensors from torch and links to libfh.so. It is rebuilt
+    for another torch or Python too: their ABI is not this project's to keep."""
     headers = [os.path.join(INCLUDE, h) for h in ("fh.h", "fh_ops.h")]
-    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= max(map(os.path.getmtime, [BIND_SRC, *headers])):
+    stamp, made_for = os.path.join(OBJ, "bind.made_for"), _bind_made_for()
+    if (not force and os.path.exists(BIND) and os.path.exists(stamp) and open(stamp).read() == made_for and
+            os.path.getmtime(BIND) >= max(map(os.path.getmtime, [BIND_SRC, *headers]))):
         return
     import sysconfig
 
@@ -89,6 +98,8 @@ def _build_bind(force: bool) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as f:
+        f.write(made_for)
 
 
 if __name__ == "__main__":
