@@ -185,6 +185,50 @@ __device__ __forceinline__ float2 inv_root(float m) {
   return make_float2(r, m > 1e-30f && m < INFINITY ? 0.5f * r * d : 0.f);
 }
 
+// A value of each of a row's W warps, joined; the same bits in all of them. One use per place in the code.
+template <int W, typename F>
+__device__ __forceinline__ float row_reduce(float x, F join) {
+  if constexpr (W > 1) {
+    __shared__ float part[W];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = part[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) x = join(x, part[w]);
+  }
+  return x;
+}
+
+// Rows whose squares leave float32's range (1e19 and above, or 1e-15 and below where eps is less than
+// 1e-30): scales them by the power of two that takes the largest to [2, 4), or by 2^127, and returns
+// mean(s^2) + eps of that, with eps scaled alike; `mean` as it was for rows of zeros, and for those with an
+// infinity or a NaN. Only they take this way: the others' times are those without it (23040 x 1536 fp32
+// and bf16 to mxfp8 63 us).
+template <int W, int NC>
+__device__ __forceinline__ float rescale_row(float (&v)[NC][8], float mean, int D, float eps) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) m = amax3(m, v[i][e], v[i][e + 1]);
+  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+  m = row_reduce<W>(m, [](float s, float t) { return amax3(s, t, 0.f); });
+  if (!(m > 0.f && m < INFINITY)) return mean;
+  const float scale = __uint_as_float(min(254u, 255u - (__float_as_uint(m) >> 23)) << 23);
+  const float small = eps * scale * scale;
+  if (!(small < INFINITY)) return mean;
+  float q = 0.f;
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[i][e] *= scale;
+      q = fmaf(v[i][e], v[i][e], q);
+    }
+  q = row_reduce<W>(warp_sum(q), [](float s, float t) { return s + t; });
+  return q / (float)D + small;
+}
+
 // Eight consecutive values as they lie in memory, zeros where `in` is false: fp32 in one access
 // where `wide` says that they lie on 32 bytes
 template <typename T>
@@ -267,16 +311,10 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
       const float2 s = make_float2(v[i][e], v[i][e + 1]);
       q2 = fma2(s, s, q2);
     }
-  float q = warp_sum(q2.x + q2.y);
-  if constexpr (W > 1) {
-    __shared__ float part[W];
-    if (lane == 0) part[warp] = q;
-    __syncthreads();
-    q = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) q += part[w];
-  }
-  const float2 rstd = inv_root(q / (float)D + eps);
+  const float q = row_reduce<W>(warp_sum(q2.x + q2.y), [](float s, float t) { return s + t; });
+  float mean = q / (float)D + eps;
+  if (!(mean >= 1e-30f && mean < INFINITY)) mean = rescale_row<W>(v, mean, D, eps);
+  const float2 rstd = inv_root(mean);
   const float2 r2 = make_float2(rstd.x, rstd.x), lo2 = make_float2(rstd.y, rstd.y);
   const long mb = ((int)row / rows_per_batch) * bstride;
 #pragma unroll
