@@ -459,9 +459,10 @@ def linear_mx(A, W, bias=None, act=None, out=None, stream=None):
     """act(A @ W^T + bias) of two MXTensors of one format, on the block-scaled tensor core.
 
     A is rows x K, W columns x K, bias float32 [columns] or None, act None or "gelu" (the tanh
-    form). The result has the type that `out` names: torch.bfloat16 (the default),
-    torch.float32, or "mxfp8" / "mxfp4" (columns a multiple of 32), an operand of the next
-    product; sums are kept in float32."""
+    form; -2.7e-9 for arguments below -5.6). The result has the type that `out` names:
+    torch.bfloat16 (the default), torch.float32, or "mxfp8" / "mxfp4" (columns a multiple of 32), an
+    operand of the next product. Sums are kept in float32, cut off by the tensor core where an addition
+    does not fit (1e-7 of the result's norm at K = 1536)."""
     bind = _bind or _load_bind()
     if stream is None:
         return bind.linear_mx(A, W, bias, act, out)

@@ -367,7 +367,8 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
 // or 12 warps of two leave the SM half empty: 6144 columns 43.4, 8 of 3 40.9); rows of bf16, half as many
 // bytes, at three or four, whichever leaves fewer lanes idle (1536 columns: 26.2 us with 2 of 3, 28.1 with
 // 3 of 2; 4000 columns: 28.5 with 4 of 4, 30.4 with 6 of 3). Up to 256 rows each is a latency (100 x 1536:
-// 2.6 us with 8 of 1, 3.0 with 4 of 2). The pairs are compiled: with the count of warps known at run time only,
+// 2.6 us with 8 of 1, 3.0 with 4 of 2). Above 8192 columns there is one pair, 16 of 4, and no other was
+// measured (2440 x 10240 fp32 5.0 TB/s, x 16384 5.6). The pairs are compiled: with the count of warps known at run time only,
 // a row's addresses cost up to a tenth (30000 x 1568 bf16 66 us, 59 compiled).
 template <typename TX, typename TR, int OUT>
 cudaError_t launch_norm(const void* x, const void* res, void* sum, const float* a, const float* c, long bstride,

@@ -139,7 +139,7 @@ def quantize(a):
 
 
 def add_rms_norm(a):
-    """fp32 rows and a bf16 branch, with one stream's scale and shift, as before a block's projection."""
+    """fp32 rows and a bf16 branch, with one stream's scale and shift."""
     import torch
     g = _gen(7)
     M, D = a.rows, a.dim

@@ -107,11 +107,13 @@ int fh_op_add_rms_norm(const void* x, int x_dtype, const void* res, int res_dtyp
 enum fh_act { FH_ACT_NONE = 0, FH_ACT_GELU = 1 };
 
 /* out [M][N] = act(A [M][K] * W [N][K]^T + bias [N]) of two microscaled operands of one type, on
- * the block-scaled tensor core, accumulated in fp32; bias float32 or null; act FH_ACT_GELU: the
- * tanh form of GELU (results for arguments below -5.6 are off by up to 3e-9). K % 32 == 0; N any, but a multiple of 32 for a microscaled out. out_type any
- * of fh_dtype; out_scales for the microscaled ones, else null. A row or column with a NaN scale
- * gives NaN results. out may not overlap the operands. FH_ERR_TIMEOUT: a kernel-side wait of an earlier
- * call on this device ran out; reported once, nothing is launched. */
+ * the block-scaled tensor core, accumulated in fp32 (it cuts off what does not fit an addition: the
+ * result's norm is off by 1e-7 at K = 1536, 3e-7 at 8960); bias float32 or null; act FH_ACT_GELU: the
+ * tanh form of GELU (-2.7e-9 for arguments below -5.6, which is off by up to that). K % 32 == 0; N any,
+ * but a multiple of 32 for a microscaled out. out_type any of fh_dtype; out_scales for the
+ * microscaled ones, else null. A row or column with a NaN scale gives NaN results. out may not overlap
+ * the operands. FH_ERR_TIMEOUT: a kernel-side wait of an earlier call on this device ran out; reported
+ * once, nothing is launched. */
 int fh_op_linear_mx(const void* A, const void* A_scales, const void* W, const void* W_scales, const float* bias,
                     int M, int N, int K, int mxtype, int act, int out_type, void* out, void* out_scales,
                     void* stream);
